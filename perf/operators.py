@@ -366,18 +366,23 @@ def _scan_bwd_plain(s):
     return dg.to(ty), (grad * w).to(ty), a[:, 0] * grad[:, 0], dfloor
 
 
-# 8-bit moments.  First: E4M3 codes times a scale per block, largest |m| at 448.  Second:
-# its root as an unsigned float of 4 exponent and 4 mantissa bits, value(c) = 2 f for e = 0
-# and (16 + f) 2^e otherwise (e = c >> 4, f = c & 15), largest root at code 254.
-TOP_M, TOP_R, TINY = 448.0, 983040.0, 2.0 ** -100
+# 8-bit moments.  First: E4M3 codes times a scale per block.  Second: its root as an unsigned
+# float of 4 exponent and 4 mantissa bits, value(c) = 2 f for e = 0 and (16 + f) 2^e
+# otherwise (e = c >> 4, f = c & 15).  The scales are powers of two that bring the block's
+# largest magnitude into [2^7, 2^8) and [2^18, 2^19).
+TINY = 2.0 ** -100
+
+
+def _scale(top, exponent):
+    """Power of two that divides top into [2^exponent, 2^(exponent + 1)); 0 below TINY."""
+    two = ((top.view(torch.int32) & 0x7F800000) - (exponent << 23)).view(F32)
+    return torch.where(top >= TINY, two, 0.0)
 
 
 def _m_encode(m):
-    top = m.abs().amax(1, keepdim=True)
-    live = top >= TINY
-    t = torch.where(live, m * (TOP_M / torch.where(live, top, 1.0)), 0.0)
-    codes = t.clamp(-TOP_M, TOP_M).to(torch.float8_e4m3fn).view(torch.uint8)
-    return codes.view(-1), torch.where(live, top / TOP_M, 0.0).view(-1)
+    scale = _scale(m.abs().amax(1, keepdim=True), 7)
+    t = torch.where(scale > 0.0, m / torch.where(scale > 0.0, scale, 1.0), 0.0)
+    return t.to(torch.float8_e4m3fn).view(torch.uint8).view(-1), scale.view(-1)
 
 
 def _m_decode(codes, scale):
@@ -386,14 +391,13 @@ def _m_decode(codes, scale):
 
 def _r_encode(r, draws):
     """draws: 16-bit numbers; the fraction of a step plus (draw + 1/2) / 2^16 carries."""
-    top = r.amax(1, keepdim=True)
-    live = top >= TINY
-    t = torch.where(live, r * (TOP_R / torch.where(live, top, 1.0)), 0.0)
+    scale = _scale(r.amax(1, keepdim=True), 18)
+    t = torch.where(scale > 0.0, r / torch.where(scale > 0.0, scale, 1.0), 0.0)
     low = t < 32.0
     bits = torch.where(low, t + 32.0, t).view(torch.int32).to(torch.int64)
     codes = ((bits - 0x42000000 + 8 * draws + 4) >> 19) + torch.where(low, 0, 16)
     codes = torch.where(t > 0.0, codes.clamp(1, 254), 0)
-    return codes.to(torch.uint8).view(-1), torch.where(live, top / TOP_R, 0.0).view(-1)
+    return codes.to(torch.uint8).view(-1), scale.view(-1)
 
 
 def _r_decode(codes, scale):
@@ -570,19 +574,22 @@ def _in_blocks(x):
     return wide.view(-1, BLOCK)
 
 
+def _unit(b, exponent):
+    top = b.abs().amax(1, keepdim=True).clamp_min(1e-300)
+    return torch.exp2(torch.floor(torch.log2(top)) - exponent)
+
+
 def _m_round(m):
     b = _in_blocks(m)
-    scale = b.abs().amax(1, keepdim=True).clamp_min(1e-300) / 448.0
-    t = b / scale
+    t = b / _unit(b, 7)
     step = torch.exp2(torch.floor(torch.log2(t.abs().clamp_min(2.0 ** -6))) - 3)
-    return (torch.round(t / step) * step * scale).view(-1)[:m.numel()]
+    return (torch.round(t / step) * step * _unit(b, 7)).view(-1)[:m.numel()]
 
 
 def _v_round(v, draws):
     b = torch.sqrt(_in_blocks(v))
-    scale = b.amax(1, keepdim=True).clamp_min(1e-300) / 983040.0
-    t = b / scale
+    t = b / _unit(b, 18)
     step = torch.exp2(torch.floor(torch.log2(t.clamp_min(32.0))) - 4)
     up = torch.floor(t / step + (_in_blocks(draws.to(F64)) + 0.5) / 65536.0)
-    r = torch.where(t > 0, (up * step).clamp(2.0, 983040.0), 0.0) * scale
+    r = torch.where(t > 0, (up * step).clamp_min(2.0), 0.0) * _unit(b, 18)
     return (r * r).view(-1)[:v.numel()]
