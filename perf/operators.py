@@ -349,7 +349,7 @@ def _scan_plain(g, u, floor, h0, reset):
 
 def _scan_bwd_plain(s):
     a, w, sg, sc = _decay(s["g"], s["floor"], s["reset"])
-    dy = s["dy"].float()
+    dy = s["dy"].to(F32, copy=True)   # (a binary32 input itself must stay as it is)
     dy[:, -1] += s["dh"]
     after = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)
     grad = _scan(after.flip(1), dy.flip(1)).flip(1)
