@@ -6,7 +6,8 @@ library is loaded from this package directory; if it is missing or cannot be loa
 call raises -- there is no other implementation to fall back to.
 
 Low-level functions carry the C names (``nvfp4_quantize`` ...) and take raw pointers;
-``quantize`` / ``dequantize`` / ``gemm`` wrap them for torch tensors.
+``quantize`` / ``dequantize`` / ``gemm`` wrap them for torch tensors.  The operators around
+the linear layers have their torch-level calls in ``norm``, ``recurrence`` and ``optim``.
 """
 from __future__ import annotations
 
@@ -40,6 +41,73 @@ class Operand(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class NormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("z_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("skip_scale", ctypes.c_float), ("branch_scale", ctypes.c_float)]
+
+
+class NormForwardArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64),
+                ("post_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("next_weight", ctypes.c_void_p),
+                ("x_out", ctypes.c_void_p), ("ld_x_out", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64),
+                ("rstd", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p)]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    _fields_ = [("x_out", ctypes.c_void_p), ("ld_x_out", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64),
+                ("post_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("next_weight", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p),
+                ("dx_out", ctypes.c_void_p), ("ld_dx_out", ctypes.c_int64),
+                ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("ld_dx", ctypes.c_int64),
+                ("dz", ctypes.c_void_p), ("ld_dz", ctypes.c_int64),
+                ("dpost_weight", ctypes.c_void_p), ("dnext_weight", ctypes.c_void_p),
+                ("dgate", ctypes.c_void_p), ("ld_dgate", ctypes.c_int64)]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("time", ctypes.c_int64), ("chan", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("g", ctypes.c_void_p), ("g_batch", ctypes.c_int64), ("g_time", ctypes.c_int64),
+                ("u", ctypes.c_void_p), ("u_batch", ctypes.c_int64), ("u_time", ctypes.c_int64),
+                ("floor", ctypes.c_void_p), ("h0", ctypes.c_void_p), ("reset", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_batch", ctypes.c_int64), ("y_time", ctypes.c_int64),
+                ("h_last", ctypes.c_void_p)]
+
+
+class ScanGradArgs(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dy_batch", ctypes.c_int64), ("dy_time", ctypes.c_int64),
+                ("dh_last", ctypes.c_void_p),
+                ("dg", ctypes.c_void_p), ("dg_batch", ctypes.c_int64), ("dg_time", ctypes.c_int64),
+                ("du", ctypes.c_void_p), ("du_batch", ctypes.c_int64), ("du_time", ctypes.c_int64),
+                ("dh0", ctypes.c_void_p), ("dfloor", ctypes.c_void_p)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("stochastic_param", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("grad_scale", ctypes.c_void_p)]
+
+
 class NVFP4Error(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -50,6 +118,11 @@ EXPORTED = ("nvfp4_quantize_workspace_bytes", "nvfp4_quantize", "nvfp4_quantize_
             "nvfp4_dequantize",
             "nvfp4_gemm", "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_ws", "nvfp4_transpose_bf16", "mxfp4_quantize", "mxfp4_dequantize",
             "mxfp4_gemm",
+            "nvfp4_residual_norm_forward", "nvfp4_residual_norm_workspace_bytes",
+            "nvfp4_residual_norm_backward", "nvfp4_gated_scan_workspace_bytes",
+            "nvfp4_gated_scan_forward", "nvfp4_gated_scan_backward",
+            "nvfp4_adamw_table_bytes", "nvfp4_adamw_table", "nvfp4_adamw_step",
+            "nvfp4_adamw_moments",
             "nvfp4_status_string", "nvfp4_abi_version")
 
 _lib = None
@@ -91,6 +164,27 @@ def load(path: str = LIB_PATH):
     L.mxfp4_dequantize.restype = ctypes.c_int
     L.mxfp4_gemm.argtypes = [P, P, P, P, i64, i64, i64, P, i64, i32, P]
     L.mxfp4_gemm.restype = ctypes.c_int
+    size, R = ctypes.c_size_t, ctypes.POINTER
+    L.nvfp4_residual_norm_forward.argtypes = [R(NormParams), R(NormForwardArgs), P]
+    L.nvfp4_residual_norm_forward.restype = ctypes.c_int
+    L.nvfp4_residual_norm_workspace_bytes.argtypes = [R(NormParams)]
+    L.nvfp4_residual_norm_workspace_bytes.restype = size
+    L.nvfp4_residual_norm_backward.argtypes = [R(NormParams), R(NormBackwardArgs), P, size, P]
+    L.nvfp4_residual_norm_backward.restype = ctypes.c_int
+    L.nvfp4_gated_scan_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.nvfp4_gated_scan_workspace_bytes.restype = size
+    L.nvfp4_gated_scan_forward.argtypes = [R(ScanArgs), P, size, P]
+    L.nvfp4_gated_scan_forward.restype = ctypes.c_int
+    L.nvfp4_gated_scan_backward.argtypes = [R(ScanArgs), R(ScanGradArgs), P, size, P]
+    L.nvfp4_gated_scan_backward.restype = ctypes.c_int
+    L.nvfp4_adamw_table_bytes.argtypes = [i64]
+    L.nvfp4_adamw_table_bytes.restype = size
+    L.nvfp4_adamw_table.argtypes = [R(AdamWTensor), i64, i32, P, size]
+    L.nvfp4_adamw_table.restype = ctypes.c_int
+    L.nvfp4_adamw_step.argtypes = [P, P, P, R(AdamWParams), P]
+    L.nvfp4_adamw_step.restype = ctypes.c_int
+    L.nvfp4_adamw_moments.argtypes = [P, P, P, P, i64, P, P, i32, P]
+    L.nvfp4_adamw_moments.restype = ctypes.c_int
     L.nvfp4_status_string.argtypes = [ctypes.c_int]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_abi_version.argtypes = []
@@ -155,6 +249,49 @@ def mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, c, ldc, out_dtype,
                stream) -> int:
     return int(load().mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, c, ldc,
                                  out_dtype, stream))
+
+
+def nvfp4_residual_norm_forward(params: NormParams, args: NormForwardArgs, stream) -> int:
+    return int(load().nvfp4_residual_norm_forward(params, args, stream))
+
+
+def nvfp4_residual_norm_workspace_bytes(params: NormParams) -> int:
+    return int(load().nvfp4_residual_norm_workspace_bytes(params))
+
+
+def nvfp4_residual_norm_backward(params: NormParams, args: NormBackwardArgs, ws, ws_bytes,
+                                 stream) -> int:
+    return int(load().nvfp4_residual_norm_backward(params, args, ws, ws_bytes, stream))
+
+
+def nvfp4_gated_scan_workspace_bytes(batch, time, chan, backward) -> int:
+    return int(load().nvfp4_gated_scan_workspace_bytes(batch, time, chan, backward))
+
+
+def nvfp4_gated_scan_forward(args: ScanArgs, ws, ws_bytes, stream) -> int:
+    return int(load().nvfp4_gated_scan_forward(args, ws, ws_bytes, stream))
+
+
+def nvfp4_gated_scan_backward(args: ScanArgs, grads: ScanGradArgs, ws, ws_bytes, stream) -> int:
+    return int(load().nvfp4_gated_scan_backward(args, grads, ws, ws_bytes, stream))
+
+
+def nvfp4_adamw_table_bytes(count) -> int:
+    return int(load().nvfp4_adamw_table_bytes(count))
+
+
+def nvfp4_adamw_table(tensors, count, state_bits, table, table_bytes) -> int:
+    return int(load().nvfp4_adamw_table(tensors, count, state_bits, table, table_bytes))
+
+
+def nvfp4_adamw_step(table, table_device, grads, params: AdamWParams, stream) -> int:
+    return int(load().nvfp4_adamw_step(table, table_device, grads, params, stream))
+
+
+def nvfp4_adamw_moments(exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, n, m_out, v_out,
+                        out_dtype, stream) -> int:
+    return int(load().nvfp4_adamw_moments(exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale,
+                                          n, m_out, v_out, out_dtype, stream))
 
 
 def nvfp4_status_string(status: int) -> str:

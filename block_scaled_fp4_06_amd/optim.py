@@ -1,0 +1,227 @@
+"""AdamW over many tensors in one launch, moments in 32 or in 8 bits.
+
+  m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+  w = w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+
+Parameters are bf16 or float32, of any size.  A bf16 parameter may have a float32 master
+copy, which then is what the update works on; without one it is rounded to nearest, or
+stochastically (``stochastic_rounding=True``: small updates survive on average).
+
+The moments of all parameters live in flat buffers (``AdamWState``), each parameter's share
+beginning at a multiple of 256 elements.  8-bit moments hold, per block of 256 elements of a
+parameter, one float32 scale (a power of two) and a byte per element: E4M3 codes for the first
+moment, and for the second the root of v as an unsigned float of 4 exponent and 4 mantissa bits, rounded
+stochastically (rounding to nearest would freeze it: beta2 near 1 moves v by less than half a
+code per step).  The draws come from Philox4x32-10 keyed on (seed, step, parameter, element),
+so a step's result is a function of its inputs alone.
+
+The step number and lr are arguments of the launch: a captured HIP graph of a step would
+repeat that step's values.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Optional
+
+from . import nvfp4 as N
+from .launch import check, dtype_code, on_stream, ptr
+
+BLOCK = 256   # elements of one block of 8-bit moments (NVFP4_ADAMW_BLOCK)
+
+
+@dataclass
+class AdamWState:
+    """Flat state of a list of parameters: parameter i's share begins at offsets(params)[i].
+
+    bits 32: exp_avg, exp_avg_sq float32.  bits 8: uint8 codes, and float32 scales per 256
+    elements.  master: float32 copies of the parameters, or None."""
+    bits: int
+    exp_avg: "object"
+    exp_avg_sq: "object"
+    exp_avg_scale: Optional["object"] = None
+    exp_avg_sq_scale: Optional["object"] = None
+    master: Optional["object"] = None
+    step: int = 0
+
+
+def offsets(params):
+    """Where each parameter's share of the flat state begins, and the state's length."""
+    at, end = [], 0
+    for p in params:
+        at.append(end)
+        end += -(-p.numel() // BLOCK) * BLOCK
+    return at, end
+
+
+def new_state(params, bits=32, master=False) -> AdamWState:
+    """Zero moments for `params`, and with master=True float32 copies of their values."""
+    import torch
+    if bits not in (32, 8):
+        raise ValueError("bits must be 32 or 8, not %r" % (bits,))
+    params = list(params)
+    if not params:
+        raise ValueError("no parameters")
+    dev = params[0].device
+    at, end = offsets(params)
+    copies = None
+    if master:
+        copies = torch.zeros(end, dtype=torch.float32, device=dev)
+        for a, p in zip(at, params):
+            copies[a:a + p.numel()].copy_(p.detach().reshape(-1))
+    if bits == 32:
+        return AdamWState(32, torch.zeros(end, dtype=torch.float32, device=dev),
+                          torch.zeros(end, dtype=torch.float32, device=dev), master=copies)
+    return AdamWState(8, torch.zeros(end, dtype=torch.uint8, device=dev),
+                      torch.zeros(end, dtype=torch.uint8, device=dev),
+                      torch.zeros(end // BLOCK, dtype=torch.float32, device=dev),
+                      torch.zeros(end // BLOCK, dtype=torch.float32, device=dev), copies)
+
+
+class AdamW:
+    """The optimizer of a fixed list of parameters (contiguous tensors on one GPU).
+
+    weight_decay: one number, or one per parameter.  state: an AdamWState to go on with;
+    by default new_state(params, bits, master).  Tensors in `state` are used, not copied."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, bits=32,
+                 master=False, state: Optional[AdamWState] = None, stochastic_rounding=False,
+                 seed=0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        self.device = self.params[0].device
+        for i, p in enumerate(self.params):
+            dtype_code("params[%d]" % i, p)
+            if p.device != self.device:
+                raise ValueError("params[%d] is on %s, expected %s" % (i, p.device, self.device))
+            if not p.is_contiguous():
+                raise ValueError("params[%d] must be contiguous" % i)
+        if not 0.0 <= betas[0] < 1.0 or not 0.0 <= betas[1] < 1.0:
+            raise ValueError("betas must lie in [0, 1), not %r" % (betas,))
+        if not eps >= 0.0:
+            raise ValueError("eps must not be negative")
+        decay = weight_decay if isinstance(weight_decay, (list, tuple)) else (
+            [weight_decay] * len(self.params))
+        if len(decay) != len(self.params):
+            raise ValueError("%d weight_decay values for %d parameters" % (len(decay),
+                                                                           len(self.params)))
+        self.lr, self.betas, self.eps = lr, tuple(betas), eps
+        self.weight_decay = [float(d) for d in decay]
+        self.stochastic_rounding, self.seed = bool(stochastic_rounding), int(seed)
+        self.state = state if state is not None else new_state(self.params, bits, master)
+        self._check_state()
+        self._shapes = [(p.shape, p.numel()) for p in self.params]
+        self._table = None
+
+    def _check_state(self):
+        import torch
+        s, (_, end) = self.state, offsets(self.params)
+        if s.bits not in (32, 8):
+            raise ValueError("state.bits must be 32 or 8, not %r" % (s.bits,))
+        kind = torch.float32 if s.bits == 32 else torch.uint8
+        N._check_buffer("state.exp_avg", s.exp_avg, (end,), (kind,), self.device, False)
+        N._check_buffer("state.exp_avg_sq", s.exp_avg_sq, (end,), (kind,), self.device, False)
+        if s.bits == 8:
+            for name in ("exp_avg_scale", "exp_avg_sq_scale"):
+                N._check_buffer("state." + name, getattr(s, name), (end // BLOCK,),
+                                (torch.float32,), self.device, False)
+        if s.master is not None:
+            N._check_buffer("state.master", s.master, (end,), (torch.float32,), self.device, False)
+
+    def _layout(self, grads):
+        """The table of tensors for gradients of these types, on the host and the device; made
+        again when a parameter's storage, the state or a gradient's type has changed."""
+        import torch
+        s = self.state
+        pins = [p.data_ptr() for p in self.params]
+        pins += [t.data_ptr() for t in (s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
+                                        s.exp_avg_sq_scale, s.master) if t is not None]
+        kinds = [self.params[i].dtype if g is None else g.dtype for i, g in enumerate(grads)]
+        if self._table is not None and self._table[0] == pins and self._table[1] == kinds:
+            return self._table
+        self._check_state()
+        count, at = len(self.params), offsets(self.params)[0]
+        rows = (N.AdamWTensor * count)()
+        width = 4 if s.bits == 32 else 1
+        for i, (p, a) in enumerate(zip(self.params, at)):
+            r = rows[i]
+            r.param, r.n = ptr(p), p.numel()
+            bf16 = p.dtype == torch.bfloat16
+            r.master = s.master.data_ptr() + 4 * a if s.master is not None and bf16 else None
+            r.exp_avg = s.exp_avg.data_ptr() + width * a
+            r.exp_avg_sq = s.exp_avg_sq.data_ptr() + width * a
+            if s.bits == 8:
+                r.exp_avg_scale = s.exp_avg_scale.data_ptr() + 4 * (a // BLOCK)
+                r.exp_avg_sq_scale = s.exp_avg_sq_scale.data_ptr() + 4 * (a // BLOCK)
+            r.weight_decay = self.weight_decay[i]
+            r.param_dtype = dtype_code("params[%d]" % i, p)
+            r.grad_dtype = 0 if kinds[i] == torch.bfloat16 else 1
+        need = N.nvfp4_adamw_table_bytes(count)
+        host = torch.empty(need, dtype=torch.uint8)
+        check(N.nvfp4_adamw_table(rows, count, s.bits, host.data_ptr(), need), "nvfp4_adamw_table")
+        self._table = (pins, kinds, host, host.to(self.device))
+        return self._table
+
+    def step(self, grads=None, lr=None, grad_scale=None, stream=None):
+        """One update.  grads: a list like params (default: each parameter's .grad), contiguous,
+        bf16 or float32; None leaves a parameter as it is.  grad_scale: a float32 tensor of one
+        element on the GPU that multiplies every gradient (clipping, loss scaling).  lr: this
+        step's (and from then on the optimizer's) learning rate."""
+        import torch
+        if grads is None:
+            grads = [p.grad for p in self.params]
+        if len(grads) != len(self.params):
+            raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
+        bf16, f32, dev, pointers = torch.bfloat16, torch.float32, self.device, []
+        for i, (g, (shape, n)) in enumerate(zip(grads, self._shapes)):
+            if g is None:
+                pointers.append(None)
+                continue
+            if g.shape != shape or not g.is_contiguous():
+                raise ValueError("grads[%d] must be a contiguous tensor of shape %s" %
+                                 (i, tuple(shape)))
+            if g.dtype is not bf16 and g.dtype is not f32:
+                raise ValueError("grads[%d] has dtype %s, expected torch.bfloat16 or "
+                                 "torch.float32" % (i, g.dtype))
+            if g.device != dev:
+                raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
+            pointers.append(g.data_ptr() if n else None)
+        if grad_scale is not None:
+            N._check_buffer("grad_scale", grad_scale.reshape(-1), (1,), (f32,), dev, False)
+        if lr is not None:
+            self.lr = lr
+        s = self.state
+        used = (*grads, grad_scale, *self.params, s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
+                s.exp_avg_sq_scale, s.master)
+        with on_stream(stream, dev, used) as handle:
+            _, _, host, device = self._layout(grads)
+            prm = N.AdamWParams(self.lr, self.betas[0], self.betas[1], self.eps, s.step + 1,
+                                self.seed, 1 if self.stochastic_rounding else 0, 0,
+                                ptr(grad_scale))
+            check(N.nvfp4_adamw_step(host.data_ptr(), device.data_ptr(),
+                                     (ctypes.c_void_p * len(pointers))(*pointers), prm, handle),
+                  "nvfp4_adamw_step")
+            device.record_stream(torch.cuda.current_stream(dev))
+        torch.autograd.graph.increment_version(self.params)
+        s.step += 1
+
+    def moments(self, dtype=None, stream=None):
+        """(m, v): the moments' values, flat as the state is; 32-bit moments themselves, 8-bit
+        ones decoded to `dtype` (float32 by default, or bf16)."""
+        import torch
+        s = self.state
+        if s.bits == 32:
+            return s.exp_avg, s.exp_avg_sq
+        dtype = dtype or torch.float32
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("dtype %s, expected torch.bfloat16 or torch.float32" % dtype)
+        codes = (s.exp_avg, s.exp_avg_scale, s.exp_avg_sq, s.exp_avg_sq_scale)
+        with on_stream(stream, self.device, codes) as handle:
+            m = torch.empty(s.exp_avg.shape, dtype=dtype, device=self.device)
+            v = torch.empty(s.exp_avg.shape, dtype=dtype, device=self.device)
+            check(N.nvfp4_adamw_moments(ptr(codes[0]), ptr(codes[1]), ptr(codes[2]), ptr(codes[3]),
+                                        m.numel(), ptr(m), ptr(v),
+                                        1 if dtype == torch.float32 else 0, handle),
+                  "nvfp4_adamw_moments")
+        return m, v

@@ -18,7 +18,8 @@
  *   - Argument errors are returned before any HIP call is made.  A failed kernel launch
  *     returns NVFP4_ERR_HIP.  Errors that depend on the data (inf/NaN input) are reported
  *     on the device: the tensor scale becomes NaN and *dev_status becomes nonzero.
- *   - Every device pointer must be 16-byte aligned; leading dimensions are in elements.
+ *   - Every device pointer must be 16-byte aligned (the operators around the linear layers,
+ *     at the end, say what they ask instead); leading dimensions are in elements.
  *   - Data pointers of an empty tensor (a zero dimension) may be NULL; the tensor scale
  *     output of nvfp4_quantize is still written (1.0).
  *   - `stream` is a hipStream_t (NULL = the default stream).
@@ -268,6 +269,221 @@ nvfp4_status mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64
 nvfp4_status mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
                         const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c,
                         int64_t ldc, int32_t out_dtype, nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Operators around the linear layers of a training step (the pages' model is a hybrid
+ * Mamba-Transformer, [NV-blog] recipe results): the norms, gate and residual sum between
+ * blocks, a gated linear recurrence over time, and the AdamW update.  All statistics,
+ * sums and states are binary32.  Sizes are arbitrary (no multiples required), pointers
+ * need only their element's alignment; 16-byte aligned rows run the wide-load kernels.
+ * ---------------------------------------------------------------------------------- */
+
+typedef enum { NVFP4_DT_BF16 = 0, NVFP4_DT_FP32 = 1 } nvfp4_dtype;
+
+/* Largest row length of the norms. */
+#define NVFP4_NORM_MAX_COLS 32768
+
+/*
+ * nvfp4_residual_norm_forward -- the end of one block and the beginning of the next:
+ *   n2    = z * rstd_post,  rstd_post = 1 / sqrt(mean(z^2) + eps)          per row
+ *   x_out = skip_scale * x + branch_scale * gate * (n2 * (weight_offset + post_weight))
+ *   h     = x_out * rstd * (weight_offset + next_weight),
+ *           rstd = 1 / sqrt(mean(x_out^2) + eps) of x_out as it is stored.
+ * With z NULL there is no branch: h is the norm of x itself, and x_out, rstd_post,
+ * post_weight and gate are NULL.  With next_weight NULL only the sum is formed, and h and
+ * rstd are NULL.  gate NULL means a gate of one.  x_out may be x itself (same row stride).
+ */
+typedef struct {
+    int64_t rows, cols;     /* cols <= NVFP4_NORM_MAX_COLS */
+    int64_t gate_rows;      /* rows of gate: 1 (a gate per channel) up to rows; row r uses
+                               gate row r / (rows / gate_rows), so it divides rows */
+    int32_t x_dtype;        /* nvfp4_dtype of x, x_out and their gradients */
+    int32_t z_dtype;        /* of z, h and their gradients; x bf16 needs z bf16 */
+    int32_t weight_dtype;   /* of post_weight, next_weight and their gradients */
+    int32_t gate_dtype;     /* of gate and its gradient */
+    float eps, weight_offset, skip_scale, branch_scale;
+} nvfp4_norm_params;
+
+typedef struct {            /* row strides (ld_*) in elements, at least cols */
+    const void *x;          /* rows x cols */
+    int64_t ld_x;
+    const void *z;          /* rows x cols, or NULL */
+    int64_t ld_z;
+    const void *post_weight;/* cols */
+    const void *gate;       /* gate_rows x cols, or NULL */
+    int64_t ld_gate;
+    const void *next_weight;/* cols, or NULL */
+    void *x_out;            /* (out) rows x cols */
+    int64_t ld_x_out;
+    void *h;                /* (out) rows x cols */
+    int64_t ld_h;
+    float *rstd;            /* (out) rows */
+    float *rstd_post;       /* (out) rows */
+} nvfp4_norm_forward_args;
+
+nvfp4_status nvfp4_residual_norm_forward(const nvfp4_norm_params *p,
+                                         const nvfp4_norm_forward_args *a,
+                                         nvfp4_stream_t stream);
+
+/*
+ * nvfp4_residual_norm_backward -- the gradients of the call above, from the tensors it
+ * stored (x_out, or x where z is NULL; rstd; rstd_post).
+ * dx_out (the gradient of the sum from elsewhere) may be NULL (zero); dh is NULL exactly
+ * when next_weight is.  dx is required, dz exactly when z is given; dpost_weight,
+ * dnext_weight and dgate may be NULL (not wanted).  dx may be dx_out itself and dz may be
+ * dh (same row strides).  The sums over rows are taken in a fixed order.
+ */
+typedef struct {
+    const void *x_out;
+    int64_t ld_x_out;
+    const void *z;
+    int64_t ld_z;
+    const void *post_weight, *gate;
+    int64_t ld_gate;
+    const void *next_weight;
+    const float *rstd, *rstd_post;
+    const void *dx_out;
+    int64_t ld_dx_out;
+    const void *dh;
+    int64_t ld_dh;
+    void *dx;               /* (out) rows x cols */
+    int64_t ld_dx;
+    void *dz;               /* (out) rows x cols */
+    int64_t ld_dz;
+    void *dpost_weight, *dnext_weight; /* (out) cols */
+    void *dgate;            /* (out) gate_rows x cols */
+    int64_t ld_dgate;
+} nvfp4_norm_backward_args;
+
+/* Bytes of device memory nvfp4_residual_norm_backward needs as its workspace (16-byte
+ * aligned, any contents); 0 for parameters that the call refuses. */
+size_t nvfp4_residual_norm_workspace_bytes(const nvfp4_norm_params *p);
+
+nvfp4_status nvfp4_residual_norm_backward(const nvfp4_norm_params *p,
+                                          const nvfp4_norm_backward_args *a, void *workspace,
+                                          size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gated_scan_forward -- a gated linear recurrence over time, per batch row and channel:
+ *   s_t = sigmoid(g_t),  a_t = floor + (1 - floor) s_t,  h_t = a_t h_{t-1} + (1 - a_t) u_t
+ * with h_0 = h0 (zero where NULL), floor in [0, 1) per channel (zero where NULL).  At a
+ * step with reset != 0, a_t = 0: h_t = u_t whatever came before (a document of a packed
+ * row begins), also where what came before is inf or NaN.  y_t = h_t, rounded to the
+ * tensor's type; the state itself is carried in binary32.  One step (time = 1) serves a
+ * decoder; h_last may be h0 itself.
+ */
+typedef struct {            /* strides (*_batch, *_time) in elements; channels are contiguous */
+    int64_t batch, time, chan;
+    int32_t dtype;          /* nvfp4_dtype of g, u, y and their gradients */
+    int32_t reserved;       /* must be 0 */
+    const void *g;
+    int64_t g_batch, g_time;
+    const void *u;
+    int64_t u_batch, u_time;
+    const float *floor;     /* chan, or NULL */
+    const float *h0;        /* batch x chan, or NULL */
+    const uint8_t *reset;   /* batch x time, or NULL */
+    void *y;                /* (out; backward: as the forward call stored it) */
+    int64_t y_batch, y_time;
+    float *h_last;          /* (out, optional) batch x chan: the state after the last step */
+} nvfp4_scan_args;
+
+/* Bytes of device memory the scan of this size needs as its workspace: forward, or with
+ * backward != 0 its gradient.  0 for sizes that the calls refuse. */
+size_t nvfp4_gated_scan_workspace_bytes(int64_t batch, int64_t time, int64_t chan,
+                                        int32_t backward);
+
+nvfp4_status nvfp4_gated_scan_forward(const nvfp4_scan_args *a, void *workspace,
+                                      size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gated_scan_backward -- with G_t = dy_t + a_{t+1} G_{t+1} (dh_last after the end):
+ *   du_t = (1 - a_t) G_t,  da_t = G_t (h_{t-1} - u_t) (0 at a reset),
+ *   dg_t = da_t (1 - floor) s_t (1 - s_t),  dfloor = sum da_t (1 - s_t),  dh0 = a_1 G_1.
+ * h_{t-1} is read from y as it was stored.  a->h_last is not used.
+ */
+typedef struct {
+    const void *dy;
+    int64_t dy_batch, dy_time;
+    const float *dh_last;   /* batch x chan, or NULL (zero) */
+    void *dg;               /* (out) */
+    int64_t dg_batch, dg_time;
+    void *du;               /* (out) */
+    int64_t du_batch, du_time;
+    float *dh0;             /* (out, optional) batch x chan */
+    float *dfloor;          /* (out, optional) chan; needs floor */
+} nvfp4_scan_grads;
+
+nvfp4_status nvfp4_gated_scan_backward(const nvfp4_scan_args *a, const nvfp4_scan_grads *d,
+                                       void *workspace, size_t workspace_bytes,
+                                       nvfp4_stream_t stream);
+
+/*
+ * AdamW over many tensors in one call:
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay) - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * w is the binary32 master copy where one is given (the parameter then receives it, rounded),
+ * else the parameter.  A bf16 parameter is rounded to nearest-even or stochastically.
+ *
+ * Moments in 32 bits, or in 8 bits over blocks of 256 elements of a tensor (the last one
+ * may be shorter), each with one binary32 scale:
+ *   first:  E4M3 code * scale, nearest-even;
+ *   second: the root r = sqrt(v) as value(code) * scale with value(c) = 2 f for e = 0 and
+ *           (16 + f) 2^e otherwise, e = c >> 4, f = c & 15; rounded stochastically (with
+ *           beta2 near 1 a step moves v by less than half a code, so rounding to nearest
+ *           would never move it), a root above zero to code 1 at least.
+ *   The scales are the powers of two that bring the block's largest magnitude into
+ *   [2^7, 2^8) and [2^18, 2^19): a code that its moment has not left is kept exactly, so
+ *   rounding adds noise only as far as the moment moves.
+ *   A moment that is not finite becomes its code's NaN (0x7F, 255) and does not enter the
+ *   block's scale.  Blocks whose largest magnitude is below 2^-100 are held as zero.
+ * Stochastic rounding draws 16 bits per element, as nvfp4_quantize does: lane i % 8 of
+ * Philox4x32-10 with key = seed and counter (lo32(i / 8), hi32(i / 8), step, 2 tensor + k),
+ * i the element's index in its tensor, tensor its index in the table, k = 0 for the second
+ * moment and 1 for the parameter.
+ */
+#define NVFP4_ADAMW_BLOCK 256
+
+typedef struct {
+    void *param;            /* (device) n elements */
+    float *master;          /* (device) n binary32 values, or NULL; only for a bf16 param */
+    void *exp_avg;          /* (device) n binary32 moments, or n codes; 16-byte aligned */
+    void *exp_avg_sq;       /* as exp_avg */
+    float *exp_avg_scale;   /* (device) one per 256 elements; NULL with 32-bit moments */
+    float *exp_avg_sq_scale;
+    int64_t n;
+    double weight_decay;
+    int32_t param_dtype, grad_dtype;
+} nvfp4_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps;
+    int64_t step;           /* 1 for the first update */
+    uint64_t seed;          /* of the stochastic rounding */
+    int32_t stochastic_param; /* 1: bf16 parameters are rounded stochastically */
+    int32_t reserved;       /* must be 0 */
+    const float *grad_scale;/* (device, optional) every gradient is multiplied by it */
+} nvfp4_adamw_params;
+
+/* The table of a fixed set of tensors: nvfp4_adamw_table checks them and writes
+ * nvfp4_adamw_table_bytes(count) bytes at `table` (host, 16-byte aligned), which the caller also copies to
+ * device memory; nvfp4_adamw_step takes both copies.  state_bits is 32 or 8. */
+size_t nvfp4_adamw_table_bytes(int64_t count);
+nvfp4_status nvfp4_adamw_table(const nvfp4_adamw_tensor *tensors, int64_t count,
+                               int32_t state_bits, void *table, size_t table_bytes);
+
+/* One update of every tensor of the table.  grads: (host array) one device pointer per
+ * tensor, n elements of its grad_dtype; NULL leaves that tensor and its moments as they are. */
+nvfp4_status nvfp4_adamw_step(const void *table, const void *table_device,
+                              const void *const *grads, const nvfp4_adamw_params *p,
+                              nvfp4_stream_t stream);
+
+/* The values of 8-bit moments: n codes of each, a scale per 256 codes, as bf16 or float
+ * (out_dtype, nvfp4_dtype). */
+nvfp4_status nvfp4_adamw_moments(const uint8_t *exp_avg, const float *exp_avg_scale,
+                                 const uint8_t *exp_avg_sq, const float *exp_avg_sq_scale,
+                                 int64_t n, void *m_out, void *v_out, int32_t out_dtype,
+                                 nvfp4_stream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *nvfp4_status_string(nvfp4_status s);
