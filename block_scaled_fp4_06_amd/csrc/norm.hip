@@ -9,190 +9,652 @@
 //   dnext = sum_rows dh n,  dpost = sum_rows branch gate D n2,
 //   dgate = sum over its rows of branch D n2 (c + post)
 //
-// Plain kernels: a workgroup per row, a thread per column of the sums over rows.
+// Bound: HBM.  Forward reads x and z and writes x_out and h; backward reads x_out, z, dx_out
+// and dh and writes dx and dz: 8 and 12 bytes per element in bf16.  So a row is read once,
+// into the registers of the threads that share it, and everything that depends on its
+// statistics is formed from there.
+//
+//  * A row belongs to `waves` waves, V * K elements to a thread (V consecutive ones per
+//    load).  Workgroups are persistent: they walk over rows, the next row's loads in flight
+//    while the current one is reduced, and the weights stay in registers.
+//  * Backward needs three sums over a row, sum t n, sum G n2 (dx_out + rstd t) and
+//    sum G n2 n: with them mean(G D n2) follows without a second reduction.
+//  * Sums over rows: with s = sum D n2 over the rows that share a gate row, dgate is
+//    branch (c + post) s and dpost gathers branch gate s, so a thread keeps s, dnext and
+//    dpost for its columns.  Each slot (a range of rows, see split_rows) leaves its sums in
+//    the workspace and a second kernel adds the slots in order: no atomics, the same bits
+//    every time.
+//  * Rows too long for that (over kMaxRow columns) take two passes: the row sums first, then
+//    strips of columns that walk down the rows.
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 
 namespace nvfp4 {
 namespace {
 
-__device__ __forceinline__ float load1(const void *p, int f32, int64_t i) {
-  return f32 ? static_cast<const float *>(p)[i]
-             : __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
+// ---------------------------------------------------------------- loads and stores
+// Every thread works on 8 consecutive elements at a time.  The 16-byte accesses are to
+// packed types, so they are single instructions at any element's alignment (rows of odd
+// length, views): one path for all strides.  Only a row's last, shorter piece goes element
+// by element.
+struct __attribute__((packed, aligned(2))) Four { uint32_t w[4]; };
+
+template <bool F32>
+struct Raw {              // 8 elements as loaded
+  static constexpr int kWords = F32 ? 8 : 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const void *p, int64_t i, int cnt) {
+    if (cnt >= 8) {
+      const Four *q = reinterpret_cast<const Four *>(static_cast<const char *>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+      for (int j = 0; j < kWords / 4; ++j) {
+        const Four v = q[j];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) w[4 * j + l] = v.w[l];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= cnt) continue;
+        if constexpr (F32) w[j] = static_cast<const uint32_t *>(p)[i + j];
+        else w[j >> 1] |= (uint32_t) static_cast<const uint16_t *>(p)[i + j] << (16 * (j & 1));
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (F32) return __uint_as_float(w[j]);
+    else return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+};
+
+template <bool F32>
+__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const float (&v)[8]) {
+  if (cnt >= 8) {
+    Four *q = reinterpret_cast<Four *>(static_cast<char *>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j) {
+      Four f;
+#pragma unroll
+      for (int l = 0; l < 4; ++l)
+        f.w[l] = F32 ? __float_as_uint(v[4 * j + l])
+                     : (uint32_t)bf16_bits_rn(v[2 * l]) | ((uint32_t)bf16_bits_rn(v[2 * l + 1]) << 16);
+      q[j] = f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= cnt) continue;
+      if constexpr (F32) static_cast<float *>(p)[i + j] = v[j];
+      else static_cast<uint16_t *>(p)[i + j] = bf16_bits_rn(v[j]);
+    }
+  }
 }
 
-__device__ __forceinline__ void store1(void *p, int f32, int64_t i, float v) {
+template <bool F32>
+__device__ __forceinline__ float rounded(float v) {
+  return F32 ? v : __uint_as_float((uint32_t)bf16_bits_rn(v) << 16);
+}
+
+// Weights and gates: parameters of either type.
+__device__ __forceinline__ void load_param(const void *p, int f32, int64_t i, int cnt, float (&v)[8]) {
+  if (f32) {
+    Raw<true> r;
+    r.zero();
+    r.load(p, i, cnt);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = r.get(j);
+  } else {
+    Raw<false> r;
+    r.zero();
+    r.load(p, i, cnt);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = r.get(j);
+  }
+}
+
+__device__ __forceinline__ void store_param(void *p, int f32, int64_t i, float v) {
   if (f32) static_cast<float *>(p)[i] = v;
   else static_cast<uint16_t *>(p)[i] = bf16_bits_rn(v);
 }
 
-__device__ __forceinline__ float round_to(int f32, float v) {
-  return f32 ? v : __uint_as_float((uint32_t)bf16_bits_rn(v) << 16);
+// ---------------------------------------------------------------- sums over a row
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL,
+                                                                   ROWS, 0xF, false));
 }
 
-// Sum over the 256 threads of a workgroup, in every thread.
-__device__ float wg_sum(float v) {
-  __shared__ float part[4];
+// Sum over the 64 lanes of a wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1, 0xF>(v);    // lane ^ 1
+  v = dpp_add<0x4E, 0xF>(v);    // lane ^ 2
+  v = dpp_add<0x141, 0xF>(v);   // the other half of 8 lanes
+  v = dpp_add<0x140, 0xF>(v);   // the other half of 16
+  v = dpp_add<0x142, 0xA>(v);   // rows 1 and 3 add rows 0 and 2
+  v = dpp_add<0x143, 0xC>(v);   // rows 2 and 3 add row 1's sum
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// Sums of N values over the waves that share a row.  `part` is used in turns (turn flips): a
+// wave writes a half again only after another sum's barrier, which every wave reaches after
+// it has read that half.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[16][N], int &turn, int waves) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (waves == 1) return;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) part[turn][wave][i] = v[i];
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = part[turn][0][i];
+  for (int w = 1; w < waves; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += part[turn][w][i];
+  turn ^= 1;
 }
 
-__global__ __launch_bounds__(256) void norm_forward_kernel(NormForward n) {
+// ---------------------------------------------------------------- forward
+// blockDim = (64 waves, rows at a time); rows at a time is 1 unless waves is 1.  HOLD: the
+// weights (and a gate shared by all rows) stay in registers and the next row is fetched
+// ahead; rows of more than 16384 columns leave no registers for either.
+template <bool XF, bool ZF, int K, bool HOLD>
+__global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
+  __shared__ float part[2][16][1];
   const nvfp4_norm_params &p = n.p;
   const nvfp4_norm_forward_args &a = n.a;
-  const int64_t row = blockIdx.x;
-  const int cols = (int)p.cols;
-  float sum = 0.0f;
-  if (a.z) {
-    for (int c = threadIdx.x; c < cols; c += 256) {
-      const float v = load1(a.z, p.z_dtype, row * a.ld_z + c);
-      sum += v * v;
+  const int cols = (int)p.cols, waves = blockDim.x >> 6, tid = threadIdx.x;
+  const int64_t rows = p.rows, step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t per_gate = rows / p.gate_rows;
+  const bool branch = a.z != nullptr, next = a.next_weight != nullptr;
+  const bool one_gate = a.gate && p.gate_rows == 1;
+  const float scale = 1.0f / (float)cols;
+  int turn = 0;
+
+  int col[K], cnt[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = (k * (int)blockDim.x + tid) * 8;
+    cnt[k] = cols - col[k];
+  }
+  // (c + post) branch [gate], and c + next
+  float wp[HOLD ? K : 1][8], wn[HOLD ? K : 1][8];
+  auto post_of = [&](int k, float (&w)[8]) {
+    load_param(a.post_weight, p.weight_dtype, col[k], cnt[k], w);
+    float g[8];
+    if (one_gate) load_param(a.gate, p.gate_dtype, col[k], cnt[k], g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = p.branch_scale * (p.weight_offset + w[j]);
+      if (one_gate) w[j] *= g[j];
     }
-    const float rp = 1.0f / sqrtf(wg_sum(sum) / (float)cols + p.eps);
-    if (threadIdx.x == 0) a.rstd_post[row] = rp;
-    const int64_t grow = row / (p.rows / p.gate_rows);
-    sum = 0.0f;
-    for (int c = threadIdx.x; c < cols; c += 256) {
-      float v = load1(a.z, p.z_dtype, row * a.ld_z + c) * rp *
-                (p.weight_offset + load1(a.post_weight, p.weight_dtype, c));
-      if (a.gate) v *= load1(a.gate, p.gate_dtype, grow * a.ld_gate + c);
-      v = round_to(p.x_dtype, p.skip_scale * load1(a.x, p.x_dtype, row * a.ld_x + c) + p.branch_scale * v);
-      store1(a.x_out, p.x_dtype, row * a.ld_x_out + c, v);
-      sum += v * v;
-    }
-  } else {
-    for (int c = threadIdx.x; c < cols; c += 256) {
-      const float v = load1(a.x, p.x_dtype, row * a.ld_x + c);
-      sum += v * v;
+  };
+  auto next_of = [&](int k, float (&w)[8]) {
+    load_param(a.next_weight, p.weight_dtype, col[k], cnt[k], w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] += p.weight_offset;
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (branch) post_of(k, wp[k]);
+      if (next) next_of(k, wn[k]);
     }
   }
-  if (!a.next_weight) return;
-  const float r = 1.0f / sqrtf(wg_sum(sum) / (float)cols + p.eps);
-  if (threadIdx.x == 0) a.rstd[row] = r;
-  const void *x = a.z ? a.x_out : a.x;
-  const int64_t ld = a.z ? a.ld_x_out : a.ld_x;
-  for (int c = threadIdx.x; c < cols; c += 256)
-    store1(a.h, p.z_dtype, row * a.ld_h + c,
-           load1(x, p.x_dtype, row * ld + c) * r *
-               (p.weight_offset + load1(a.next_weight, p.weight_dtype, c)));
+
+  Raw<XF> rx[K];
+  Raw<ZF> rz[K];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      rx[k].zero();
+      rz[k].zero();
+      rx[k].load(a.x, row * a.ld_x + col[k], cnt[k]);
+      if (branch) rz[k].load(a.z, row * a.ld_z + col[k], cnt[k]);
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (HOLD && row < rows) fetch(row);
+  for (; row < rows; row += step) {
+    if (!HOLD) fetch(row);
+    float x[K][8];
+    Raw<ZF> z[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      z[k] = rz[k];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[k][j] = rx[k].get(j);
+    }
+    if (HOLD && row + step < rows) fetch(row + step);
+    if (branch) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] += z[k].get(j) * z[k].get(j);
+      row_sum<1>(s, part, turn, waves);
+      const float rp = 1.0f / sqrtf(s[0] * scale + p.eps);
+      if (tid == 0) a.rstd_post[row] = rp;
+      const int64_t grow = a.gate && !one_gate ? row / per_gate : 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float w[8], g[8];
+        if constexpr (HOLD) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = wp[k][j];
+        } else {
+          post_of(k, w);
+        }
+        if (a.gate && !one_gate) {
+          load_param(a.gate, p.gate_dtype, grow * a.ld_gate + col[k], cnt[k], g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] *= g[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[k][j] = rounded<XF>(p.skip_scale * x[k][j] + z[k].get(j) * rp * w[j]);
+        store<XF>(a.x_out, row * a.ld_x_out + col[k], cnt[k], x[k]);
+      }
+    }
+    if (!next) continue;
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[0] += x[k][j] * x[k][j];
+    row_sum<1>(s, part, turn, waves);
+    const float r = 1.0f / sqrtf(s[0] * scale + p.eps);
+    if (tid == 0) a.rstd[row] = r;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float w[8];
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = wn[k][j];
+      } else {
+        next_of(k, w);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = x[k][j] * r * w[j];
+      store<ZF>(a.h, row * a.ld_h + col[k], cnt[k], w);
+    }
+  }
 }
 
-// The terms of one element of the backward pass.
-struct Terms {
-  float t, n, d0, n2, g, w;   // d0 = dx_out; g = branch * gate; w = c + post
+// ---------------------------------------------------------------- backward
+constexpr int kMaxRow = 8192;     // columns of a row that one workgroup holds: 1024 x 8
+
+// How the rows are shared out among slots.  A slot has whole groups (rows that share a gate
+// row), or, where groups are fewer than the slots wanted, an even part of one group.
+struct Split {
+  int64_t rows, groups, slots;
+  int parts;        // slots per group; 1: a slot has whole groups
 };
 
-__device__ __forceinline__ Terms terms(const NormBackward &b, int64_t row, int64_t grow, int c,
-                                       float r, float rp) {
-  const nvfp4_norm_params &p = b.p;
-  const nvfp4_norm_backward_args &a = b.a;
-  Terms e = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (a.next_weight) {
-    e.n = load1(a.x_out, p.x_dtype, row * a.ld_x_out + c) * r;
-    e.t = load1(a.dh, p.z_dtype, row * a.ld_dh + c) *
-          (p.weight_offset + load1(a.next_weight, p.weight_dtype, c));
+__host__ __device__ inline Split split_rows(int64_t rows, int64_t groups, int64_t want) {
+  Split s = {rows, groups, 0, 1};
+  if (want > rows) want = rows;
+  if (groups >= want) {
+    s.slots = want;
+  } else {
+    const int64_t per = rows / groups;
+    int64_t parts = (want + groups - 1) / groups;
+    s.parts = (int)(parts < per ? parts : per);
+    s.slots = groups * s.parts;
   }
-  if (a.dx_out) e.d0 = load1(a.dx_out, p.x_dtype, row * a.ld_dx_out + c);
-  if (a.z) {
-    e.n2 = load1(a.z, p.z_dtype, row * a.ld_z + c) * rp;
-    e.w = p.weight_offset + load1(a.post_weight, p.weight_dtype, c);
-    e.g = p.branch_scale * (a.gate ? load1(a.gate, p.gate_dtype, grow * a.ld_gate + c) : 1.0f);
-  }
-  return e;
+  return s;
 }
 
-// The two means of a row, into the workspace.
-__global__ __launch_bounds__(256) void norm_means_kernel(NormBackward b) {
-  const nvfp4_norm_params &p = b.p;
-  const int64_t row = blockIdx.x, grow = row / (p.rows / p.gate_rows);
-  const int cols = (int)p.cols;
-  const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
-  float s = 0.0f;
-  for (int c = threadIdx.x; c < cols; c += 256) {
-    const Terms e = terms(b, row, grow, c, r, rp);
-    s += e.t * e.n;
-  }
-  const float m1 = wg_sum(s) / (float)cols;
-  s = 0.0f;
-  for (int c = threadIdx.x; c < cols; c += 256) {
-    const Terms e = terms(b, row, grow, c, r, rp);
-    s += e.g * e.w * (e.d0 + r * (e.t - e.n * m1)) * e.n2;
-  }
-  const float m2 = wg_sum(s) / (float)cols;
-  if (threadIdx.x == 0) {
-    static_cast<float *>(b.ws)[2 * row] = m1;
-    static_cast<float *>(b.ws)[2 * row + 1] = m2;
+__device__ __forceinline__ void slot_rows(const Split &s, int64_t slot, int64_t &r0, int64_t &r1) {
+  const int64_t per = s.rows / s.groups;
+  if (s.parts == 1) {
+    r0 = slot * s.groups / s.slots * per;
+    r1 = (slot + 1) * s.groups / s.slots * per;
+  } else {
+    const int64_t g = slot / s.parts, i = slot % s.parts;
+    r0 = g * per + i * per / s.parts;
+    r1 = g * per + (i + 1) * per / s.parts;
   }
 }
 
-__global__ __launch_bounds__(64) void norm_columns_kernel(NormBackward b) {
-  const nvfp4_norm_params &p = b.p;
-  const nvfp4_norm_backward_args &a = b.a;
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= p.cols) return;
-  const float *means = static_cast<const float *>(b.ws);
-  const int64_t q = p.rows / p.gate_rows;
-  float next = 0.0f, post = 0.0f, gate = 0.0f;
-  for (int64_t row = 0; row < p.rows; ++row) {
-    const float r = a.next_weight ? a.rstd[row] : 0.0f, rp = a.z ? a.rstd_post[row] : 0.0f;
-    const Terms e = terms(b, row, row / q, c, r, rp);
-    const float d = e.d0 + r * (e.t - e.n * means[2 * row]);
-    if (a.next_weight) next += load1(a.dh, p.z_dtype, row * a.ld_dh + c) * e.n;
-    post += e.g * d * e.n2;
-    gate += p.branch_scale * d * (e.n2 * e.w);
-    if ((row + 1) % q == 0) {
-      if (a.dgate) store1(a.dgate, p.gate_dtype, row / q * a.ld_dgate + c, gate);
-      gate = 0.0f;
+// What a thread keeps for its 8 columns: c + next; G = branch gate (c + post) of the current
+// group; and the sums over rows.
+struct Columns {
+  float wn[8], g[8];
+  float next[8], post[8], s[8];
+};
+
+template <bool XF, bool ZF>
+struct Operands {         // one row's
+  Raw<XF> x, d;
+  Raw<ZF> z, h;
+};
+
+// Slots' sums in the workspace: [dnext, dpost, dgate][slot][column].
+__device__ __forceinline__ float *slot_sums(void *ws, const Split &s, int which, int64_t slot, int cols) {
+  return static_cast<float *>(ws) + ((int64_t)which * s.slots + slot) * cols;
+}
+
+template <bool XF, bool ZF>
+__device__ __forceinline__ void fetch_row(const nvfp4_norm_backward_args &a, int64_t row, int col,
+                                          int cnt, Operands<XF, ZF> &o) {
+  o.x.zero(); o.d.zero(); o.z.zero(); o.h.zero();
+  o.x.load(a.x_out, row * a.ld_x_out + col, cnt);
+  if (a.z) o.z.load(a.z, row * a.ld_z + col, cnt);
+  if (a.dx_out) o.d.load(a.dx_out, row * a.ld_dx_out + col, cnt);
+  if (a.next_weight) o.h.load(a.dh, row * a.ld_dh + col, cnt);
+}
+
+// branch gate and c + post of a group (both zero without a branch).
+__device__ __forceinline__ void gate_and_post(const NormBackward &b, int64_t group, int col, int cnt,
+                                              float (&g)[8], float (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = w[j] = 0.0f;
+  if (!b.a.z) return;
+  load_param(b.a.post_weight, b.p.weight_dtype, col, cnt, w);
+  if (b.a.gate) load_param(b.a.gate, b.p.gate_dtype, group * b.a.ld_gate + col, cnt, g);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w[j] += b.p.weight_offset;
+    g[j] = b.a.gate ? b.p.branch_scale * g[j] : b.p.branch_scale;
+  }
+}
+
+__device__ __forceinline__ void open_group(const NormBackward &b, int64_t group, int col, int cnt,
+                                           Columns &c) {
+  float g[8], w[8];
+  gate_and_post(b, group, col, cnt, g, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c.g[j] = g[j] * w[j];
+    c.s[j] = 0.0f;
+  }
+}
+
+__device__ __forceinline__ void open_slot(const NormBackward &b, int64_t group, int col, int cnt,
+                                          Columns &c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c.wn[j] = c.next[j] = c.post[j] = 0.0f;
+  if (b.a.next_weight) {
+    load_param(b.a.next_weight, b.p.weight_dtype, col, cnt, c.wn);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c.wn[j] += b.p.weight_offset;
+  }
+  open_group(b, group, col, cnt, c);
+}
+
+// The end of a group, or of a slot inside one: s goes into dpost and the gate's gradient.
+__device__ __forceinline__ void close_group(const NormBackward &b, const Split &s, int64_t slot,
+                                            int64_t group, int col, int cnt, Columns &c) {
+  float g[8], w[8];
+  gate_and_post(b, group, col, cnt, g, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c.post[j] += g[j] * c.s[j];
+    const float dg = b.p.branch_scale * w[j] * c.s[j];
+    if (!b.a.dgate || j >= cnt) continue;
+    if (s.parts == 1) store_param(b.a.dgate, b.p.gate_dtype, group * b.a.ld_dgate + col + j, dg);
+    else slot_sums(b.ws, s, 2, slot, (int)b.p.cols)[col + j] = dg;
+  }
+}
+
+__device__ __forceinline__ void close_slot(const NormBackward &b, const Split &s, int64_t slot, int col,
+                                           int cnt, const Columns &c) {
+  if (b.a.dnext_weight) store<true>(slot_sums(b.ws, s, 0, slot, (int)b.p.cols), col, cnt, c.next);
+  if (b.a.dpost_weight) store<true>(slot_sums(b.ws, s, 1, slot, (int)b.p.cols), col, cnt, c.post);
+}
+
+// A thread's share of the three row sums.
+template <bool XF, bool ZF>
+__device__ __forceinline__ void partial_sums(const Operands<XF, ZF> &o, const Columns &c, float r,
+                                             float rp, float (&s)[3]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float n = o.x.get(j) * r, t = o.h.get(j) * c.wn[j];
+    const float q = c.g[j] * (o.z.get(j) * rp);
+    s[0] += t * n;
+    s[1] += q * (o.d.get(j) + r * t);
+    s[2] += q * n;
+  }
+}
+
+// dx and dz of one row, and its terms of the sums over rows.  m1 = mean(t n) and
+// m2 = mean(G D n2).
+template <bool XF, bool ZF>
+__device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, const Operands<XF, ZF> &o,
+                                           int col, int cnt, float r, float rp, float m1, float m2,
+                                           Columns &c) {
+  const float skip = b.a.z ? b.p.skip_scale : 1.0f;
+  float dx[8], dz[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float n = o.x.get(j) * r, dh = o.h.get(j), n2 = o.z.get(j) * rp;
+    const float d = o.d.get(j) + r * (dh * c.wn[j] - n * m1);
+    c.next[j] += dh * n;
+    c.s[j] += d * n2;
+    dx[j] = skip * d;
+    dz[j] = rp * (c.g[j] * d - n2 * m2);
+  }
+  store<XF>(b.a.dx, row * b.a.ld_dx + col, cnt, dx);
+  if (b.a.z) store<ZF>(b.a.dz, row * b.a.ld_dz + col, cnt, dz);
+}
+
+// Walks the rows of a slot: row(row, operands, columns) for each, the next row's operands in
+// flight, and the groups' ends between them.
+template <bool XF, bool ZF, class Row>
+__device__ __forceinline__ void walk_slot(const NormBackward &b, const Split &sp, int64_t slot, int col,
+                                          int cnt, Row &&do_row) {
+  const int64_t per = sp.rows / sp.groups;
+  int64_t row, end;
+  slot_rows(sp, slot, row, end);
+  int64_t group = row / per, left = (group + 1) * per - row;   // rows of the group from here on
+  Columns c;
+  open_slot(b, group, col, cnt, c);
+  Operands<XF, ZF> o, ahead;
+  fetch_row(b.a, row, col, cnt, ahead);
+  for (; row < end; ++row) {
+    o = ahead;
+    if (row + 1 < end) fetch_row(b.a, row + 1, col, cnt, ahead);
+    do_row(row, o, c);
+    if (--left == 0 || row + 1 == end) {
+      close_group(b, sp, slot, group, col, cnt, c);
+      if (row + 1 < end) {
+        open_group(b, ++group, col, cnt, c);
+        left = per;
+      }
     }
   }
-  if (a.dnext_weight) store1(a.dnext_weight, p.weight_dtype, c, next);
-  if (a.dpost_weight) store1(a.dpost_weight, p.weight_dtype, c, post);
-  if (p.rows == 0 && a.dgate)
-    for (int64_t g = 0; g < p.gate_rows; ++g) store1(a.dgate, p.gate_dtype, g * a.ld_dgate + c, 0.0f);
+  close_slot(b, sp, slot, col, cnt, c);
 }
 
-__global__ __launch_bounds__(256) void norm_backward_kernel(NormBackward b) {
-  const nvfp4_norm_params &p = b.p;
-  const nvfp4_norm_backward_args &a = b.a;
-  const int64_t row = blockIdx.x, grow = row / (p.rows / p.gate_rows);
-  const float r = a.next_weight ? a.rstd[row] : 0.0f, rp = a.z ? a.rstd_post[row] : 0.0f;
-  const float m1 = static_cast<const float *>(b.ws)[2 * row], m2 = static_cast<const float *>(b.ws)[2 * row + 1];
-  for (int c = threadIdx.x; c < p.cols; c += 256) {
-    const Terms e = terms(b, row, grow, c, r, rp);
-    const float d = e.d0 + r * (e.t - e.n * m1);
-    store1(a.dx, p.x_dtype, row * a.ld_dx + c, a.z ? p.skip_scale * d : d);
-    if (a.z) store1(a.dz, p.z_dtype, row * a.ld_dz + c, rp * (e.g * e.w * d - e.n2 * m2));
+// A row per workgroup (or per wave, blockDim.y of them) at a time, a slot per workgroup (or
+// wave).  THREADS bounds the workgroup: fewer threads leave more registers to each.
+template <bool XF, bool ZF, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, Split sp) {
+  __shared__ float part[2][16][3];
+  const int cols = (int)b.p.cols, waves = blockDim.x >> 6;
+  const int64_t slot = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (slot >= sp.slots) return;   // (a whole wave where blockDim.y > 1; never otherwise)
+  const float scale = 1.0f / (float)cols;
+  const int col = (int)threadIdx.x * 8, cnt = cols - col;
+  int turn = 0;
+  walk_slot<XF, ZF>(b, sp, slot, col, cnt, [&](int64_t row, const Operands<XF, ZF> &o, Columns &c) {
+    const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    partial_sums(o, c, r, rp, s);
+    row_sum<3>(s, part, turn, waves);
+    const float m1 = s[0] * scale, m2 = (s[1] - r * m1 * s[2]) * scale;
+    finish_row(b, row, o, col, cnt, r, rp, m1, m2, c);
+  });
+}
+
+// Long rows, first pass: m1 and m2 of every row, a workgroup per row at a time.
+template <bool XF, bool ZF>
+__global__ __launch_bounds__(512) void norm_means_kernel(NormBackward b, float *means) {
+  __shared__ float part[2][16][3];
+  const int cols = (int)b.p.cols, waves = blockDim.x >> 6;
+  const int64_t per = b.p.rows / b.p.gate_rows;
+  const float scale = 1.0f / (float)cols;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < b.p.rows; row += gridDim.x) {
+    const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    for (int col = (int)threadIdx.x * 8; col < cols; col += (int)blockDim.x * 8) {
+      Operands<XF, ZF> o;
+      fetch_row(b.a, row, col, cols - col, o);
+      Columns c;
+      open_slot(b, row / per, col, cols - col, c);
+      partial_sums(o, c, r, rp, s);
+    }
+    row_sum<3>(s, part, turn, waves);
+    const float m1 = s[0] * scale;
+    if (threadIdx.x == 0) {
+      means[2 * row] = m1;
+      means[2 * row + 1] = (s[1] - r * m1 * s[2]) * scale;
+    }
   }
+}
+
+// Long rows, second pass: a strip of 2048 columns of one slot's rows per workgroup.
+template <bool XF, bool ZF>
+__global__ __launch_bounds__(256) void norm_strips_kernel(NormBackward b, Split sp, const float *means,
+                                                          int strips) {
+  const int64_t slot = blockIdx.x / strips;
+  const int col = (int)((blockIdx.x % strips) * 256 + threadIdx.x) * 8, cnt = (int)b.p.cols - col;
+  if (cnt <= 0) return;
+  walk_slot<XF, ZF>(b, sp, slot, col, cnt, [&](int64_t row, const Operands<XF, ZF> &o, Columns &c) {
+    const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
+    finish_row(b, row, o, col, cnt, r, rp, means[2 * row], means[2 * row + 1], c);
+  });
+}
+
+// The slots' sums added in order.  A workgroup has 32 columns of one result, 32 threads to a
+// column, each with a consecutive share of the slots: results 0 and 1 are dnext and dpost,
+// 2 + g the gate row g.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(NormBackward b, Split sp, int strips) {
+  __shared__ float part[32][32];
+  const int cols = (int)b.p.cols, lane = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int c = (int)(blockIdx.x % strips) * 32 + lane;
+  const int64_t what = blockIdx.x / strips;
+  void *out = what == 0 ? b.a.dnext_weight : what == 1 ? b.a.dpost_weight : b.a.dgate;
+  if (!out) return;   // (the whole workgroup)
+  const int64_t first = what < 2 ? 0 : (what - 2) * sp.parts, count = what < 2 ? sp.slots : sp.parts;
+  const float *sums = slot_sums(b.ws, sp, what < 2 ? (int)what : 2, first, cols);
+  float v = 0.0f;
+  if (c < cols) {
+    const int64_t end = count * (share + 1) / 32;
+#pragma unroll 8
+    for (int64_t i = count * share / 32; i < end; ++i) v += sums[i * cols + c];
+  }
+  part[share][lane] = v;
+  __syncthreads();
+  if (share || c >= cols) return;
+  v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) v += part[w][lane];
+  if (what < 2) store_param(out, b.p.weight_dtype, c, v);
+  else store_param(out, b.p.gate_dtype, (what - 2) * b.a.ld_dgate + c, v);
+}
+
+// No rows: every sum over rows is zero.
+__global__ __launch_bounds__(256) void norm_zero_kernel(NormBackward b) {
+  const int64_t n = b.p.cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * b.p.gate_rows; i += 256 * (int64_t)gridDim.x) {
+    if (b.a.dgate) store_param(b.a.dgate, b.p.gate_dtype, i / n * b.a.ld_dgate + i % n, 0.0f);
+    if (i < n && b.a.dnext_weight) store_param(b.a.dnext_weight, b.p.weight_dtype, i, 0.0f);
+    if (i < n && b.a.dpost_weight) store_param(b.a.dpost_weight, b.p.weight_dtype, i, 0.0f);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+constexpr int kCus = 256;
+
+// Waves that share a row of `cols` columns, `each` to a thread.
+int waves_of(int64_t cols, int each) { return (int)((cols + 64 * each - 1) / (64 * each)); }
+
+// Workgroups at a time on a CU of `threads` threads whose kernels use up to 128 registers.
+int resident(int threads) { return threads >= 1024 ? 1 : 1024 / threads; }
+
+int64_t slots_wanted(const nvfp4_norm_params &p) {
+  if (p.cols > kMaxRow) return 128;
+  const int waves = waves_of(p.cols, 8);
+  return (int64_t)kCus * (waves == 1 ? 4 : resident(64 * waves));
+}
+
+Split split_of(const nvfp4_norm_params &p) { return split_rows(p.rows, p.gate_rows, slots_wanted(p)); }
+
+template <bool XF, bool ZF, int K, bool HOLD>
+hipError_t run_forward(const NormForward &n, hipStream_t stream) {
+  const int waves = waves_of(n.p.cols, 8 * K), y = waves == 1 ? 4 : 1;
+  const int64_t want = (n.p.rows + y - 1) / y, most = (int64_t)kCus * 2 * resident(64 * waves * y);
+  norm_forward_kernel<XF, ZF, K, HOLD>
+      <<<(uint32_t)(want < most ? want : most), dim3(64 * waves, y), 0, stream>>>(n);
+  return hipGetLastError();
+}
+
+template <bool XF, bool ZF>
+hipError_t forward_of(const NormForward &n, hipStream_t stream) {
+  // as few elements per thread as 1024 threads allow
+  if (n.p.cols <= 8192) return run_forward<XF, ZF, 1, true>(n, stream);
+  if (n.p.cols <= 16384) return run_forward<XF, ZF, 2, true>(n, stream);
+  return run_forward<XF, ZF, 4, false>(n, stream);
+}
+
+template <bool XF, bool ZF>
+hipError_t backward_of(const NormBackward &b, const Split &sp, hipStream_t stream) {
+  if (b.p.cols <= kMaxRow) {
+    const int waves = waves_of(b.p.cols, 8), y = waves == 1 ? 4 : 1;
+    const uint32_t grid = (uint32_t)((sp.slots + y - 1) / y);
+    if (waves <= 10)
+      norm_backward_kernel<XF, ZF, 640><<<grid, dim3(64 * waves, y), 0, stream>>>(b, sp);
+    else
+      norm_backward_kernel<XF, ZF, 1024><<<grid, dim3(64 * waves, y), 0, stream>>>(b, sp);
+    return hipGetLastError();
+  }
+  float *means = static_cast<float *>(b.ws) + 3 * sp.slots * b.p.cols;
+  const int64_t wgs = b.p.rows < 4 * kCus ? b.p.rows : 4 * kCus;
+  norm_means_kernel<XF, ZF><<<(uint32_t)wgs, 512, 0, stream>>>(b, means);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int strips = (int)((b.p.cols + 2047) / 2048);
+  norm_strips_kernel<XF, ZF><<<(uint32_t)(sp.slots * strips), 256, 0, stream>>>(b, sp, means, strips);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t norm_workspace_bytes(const nvfp4_norm_params &p) { return 8 * (size_t)p.rows; }
-
-hipError_t launch_norm_forward(const NormForward &n, hipStream_t stream) {
-  norm_forward_kernel<<<(uint32_t)n.p.rows, 256, 0, stream>>>(n);
-  return hipGetLastError();
+size_t norm_workspace_bytes(const nvfp4_norm_params &p) {
+  const Split s = split_of(p);
+  return 4 * (3 * (size_t)s.slots * (size_t)p.cols + (p.cols > kMaxRow ? 2 * (size_t)p.rows : 0));
 }
 
-hipError_t launch_norm_backward(const NormBackward &n, hipStream_t stream) {
-  hipError_t e = hipSuccess;
-  if (n.p.rows > 0) {
-    norm_means_kernel<<<(uint32_t)n.p.rows, 256, 0, stream>>>(n);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+hipError_t launch_norm_forward(const NormForward &n, hipStream_t stream) {
+  if (n.p.x_dtype == NVFP4_DT_BF16) return forward_of<false, false>(n, stream);
+  return n.p.z_dtype == NVFP4_DT_BF16 ? forward_of<true, false>(n, stream) : forward_of<true, true>(n, stream);
+}
+
+hipError_t launch_norm_backward(const NormBackward &b, hipStream_t stream) {
+  const bool sums = b.a.dnext_weight || b.a.dpost_weight || b.a.dgate;
+  if (b.p.rows == 0) {
+    if (sums) norm_zero_kernel<<<64, 256, 0, stream>>>(b);
+    return hipGetLastError();
   }
-  if (n.a.dnext_weight || n.a.dpost_weight || n.a.dgate) {
-    norm_columns_kernel<<<(uint32_t)((n.p.cols + 63) / 64), 64, 0, stream>>>(n);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (n.p.rows > 0) {
-    norm_backward_kernel<<<(uint32_t)n.p.rows, 256, 0, stream>>>(n);
-    e = hipGetLastError();
-  }
-  return e;
+  const Split sp = split_of(b.p);
+  const hipError_t e = b.p.x_dtype == NVFP4_DT_BF16   ? backward_of<false, false>(b, sp, stream)
+                       : b.p.z_dtype == NVFP4_DT_BF16 ? backward_of<true, false>(b, sp, stream)
+                                                      : backward_of<true, true>(b, sp, stream);
+  if (e != hipSuccess || !sums) return e;
+  const int strips = (int)((b.p.cols + 31) / 32);
+  const int64_t results = 2 + (b.a.dgate && sp.parts > 1 ? sp.groups : 0);
+  norm_columns_kernel<<<(uint32_t)(results * strips), 1024, 0, stream>>>(b, sp, strips);
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4
