@@ -191,7 +191,8 @@ def test_saturated_gates():
     g[:, 500] = float("-inf")
     g[0, 600], g[1, 600] = 500.0, -500.0
     y, _ = check_forward(g, u, fl, h0, None)
-    assert torch.equal(y[:, 99], y[:, 399])
+    # (both are within check_forward's bound of the same value, under 100 u of its size each)
+    assert float((y[:, 99] - y[:, 399]).abs().max()) <= 200 * U * float(y[:, 99].abs().max())
     d = check_backward(rnd((2, 700, 16), F32, 8), g, u, y, fl, h0, None, rnd((2, 16), F32, 9))
     assert bool((d.du[:, 100:400] == 0).all()) and bool((d.dg[:, 100:400] == 0).all())
 
