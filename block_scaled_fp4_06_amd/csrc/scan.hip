@@ -8,20 +8,16 @@
 //   dg = da (1 - floor) s (1 - s),  dfloor = sum da (1 - s),  dh0 = c_1
 //
 // Bound: HBM.  Forward reads g and u and writes y, 6 bytes per element in bf16; backward
-// reads dy, g, u, y and writes dg and du, 12 bytes.  One pass over the data:
+// reads dy, g, u, y and writes dg and du, 12 bytes.
 //
-//  * A tile is 128 bytes of channels (8 lanes of 16 bytes) by kGroups x S time steps: each of
-//    256 threads holds S consecutive steps of its channels in registers.  A run of steps acts
-//    on the state as h -> A h + B; the threads' (A, B) are composed through LDS, and the tile
-//    needs one state per channel from the tile before it.
-//  * That state comes over a chain of tiles.  A tile publishes its own (A, B) as soon as it
-//    has it, and its final state once it knows its first.  A tile that waits reads its last
-//    kWindow predecessors at once, takes the nearest final state and applies the (A, B) of
-//    the tiles since in order: h_j = A_j h_{j-1} + B_j whoever computes it, so the result does
-//    not depend on timing.
-//  * Workgroups take tiles from a counter, time-major, and wait only for tiles with a
-//    smaller number, which another workgroup is working on already: some workgroup can
-//    always go on, however many of them are resident.
+//  * A tile is 128 bytes of channels (8 lanes of 16 bytes) by kTile time steps: each of 256
+//    threads holds kSteps consecutive steps of its channels in registers.  A run of steps
+//    acts on the state as h -> A h + B; the threads' (A, B) are composed through LDS.
+//  * A sequence longer than a tile takes three kernels: the first forms every tile's (A, B)
+//    from g and u (backward: g and dy), the second walks over each channel's tiles and
+//    leaves the state before each, the third does the tiles.  What the first read is largely
+//    still in the 256 MB cache beside the memory when the third reads it again.  No
+//    workgroup waits for another, and every sum has one order.
 //  * A reset is a cut, not a product with zero: (cut, B) composed with anything before it is
 //    (cut, B), so inf and NaN end there.  A cut is held as A = -0.0, which no product of the
 //    other factors (in [0, 1], or NaN) gives.
@@ -36,9 +32,7 @@ namespace {
 constexpr int kGroups = 32;          // time groups of a tile: 256 threads / 8 lanes of channels
 constexpr int kSteps = 4;            // steps of a thread
 constexpr int kTile = kGroups * kSteps;
-constexpr int kWindow = 8;           // predecessors read at once
 constexpr int kShort = 16;           // steps that one thread walks over by itself
-constexpr uint64_t kWaitTicks = 500000000ull;   // last resort: 5 s of the 100 MHz clock
 
 // ---------------------------------------------------------------- loads and stores
 // 16 bytes of channels, at any element's alignment (the packed type makes them single
@@ -94,17 +88,27 @@ __device__ __forceinline__ void store(void *p, int64_t i, int cnt, const float (
 // V binary32 values (floor, states); zero where there are none.
 template <int V>
 __device__ __forceinline__ void load_f32(const float *p, int64_t i, int cnt, float (&v)[V]) {
+  if (p && cnt >= V) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = p && j < cnt ? p[i + j] : 0.0f;
+    for (int j = 0; j < V; j += 4) {
+      Raw<true> r;
+      r.load(p, i + j, 4);
+#pragma unroll
+      for (int l = 0; l < 4; ++l) v[j + l] = r.get(l);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = p && j < cnt ? p[i + j] : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------- arithmetic
-// sigmoid(g) and sigmoid(-g), each without cancellation: e = exp(-|g|) cannot overflow.
+// sigmoid(g) and sigmoid(-g), neither by a difference of near equals: for g < 0, where
+// exp(-g) may overflow (then sigmoid(g) is zero), 1 - sigmoid(g) loses nothing.
 __device__ __forceinline__ void sigmoids(float g, float &s, float &sc) {
-  const float e = __expf(-fabsf(g));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
-  s = g >= 0.0f ? r : er;
-  sc = g >= 0.0f ? er : r;
+  const float e = __expf(-g);
+  s = __builtin_amdgcn_rcpf(1.0f + e);
+  sc = g < 0.0f ? 1.0f - s : e * s;
 }
 
 __device__ __forceinline__ float cut_mark() { return -0.0f; }
@@ -112,86 +116,36 @@ __device__ __forceinline__ bool is_cut(float a) { return __float_as_uint(a) == 0
 
 struct Pair { float a, b; };   // h -> a h + b, or h -> b behind a cut
 
-__device__ __forceinline__ float apply(const Pair &p, float h) { return is_cut(p.a) ? p.b : __builtin_fmaf(p.a, h, p.b); }
-
-// First p, then q.
-__device__ __forceinline__ Pair then(const Pair &p, const Pair &q) {
-  if (is_cut(q.a)) return q;
-  return Pair{is_cut(p.a) ? p.a : q.a * p.a, __builtin_fmaf(q.a, p.b, q.b)};
+__device__ __forceinline__ float apply(const Pair &p, float h) {
+  return is_cut(p.a) ? p.b : __builtin_fmaf(p.a, h, p.b);
 }
 
-// ---------------------------------------------------------------- the chain of tiles
-// Words that have not been published are all ones; a published value that happens to be
-// (a NaN) is replaced by another NaN.
-struct Chain {
-  uint32_t *ticket;
-  uint64_t *pairs;      // [strip][chunk][channel]
-  uint32_t *states;     // [strip][chunk][channel]
-  int64_t strips, chunks, tiles, chan_strips;
+// First p, then q.  (A factor in [0, 1] times -0.0 is -0.0: what follows a cut keeps it.)
+__device__ __forceinline__ Pair then(const Pair &p, const Pair &q) {
+  return is_cut(q.a) ? q : Pair{q.a * p.a, __builtin_fmaf(q.a, p.b, q.b)};
+}
+
+// ---------------------------------------------------------------- tiles
+// Tiles along time of every sequence, and what passes between the kernels: a pair per tile
+// (but the last) and channel, the state before every tile.
+struct Tiling {
+  int64_t chunks;
+  Pair *pairs;        // [batch][chunk][channel]
+  float *states;      // [batch][chunk][channel]
 };
 
-constexpr uint64_t kNoPair = ~0ull;
-constexpr uint32_t kNoState = ~0u;
-
-__device__ __forceinline__ void publish(uint64_t *at, const Pair &p) {
-  uint64_t w = ((uint64_t)__float_as_uint(p.b) << 32) | __float_as_uint(p.a);
-  if (w == kNoPair) w = (0x7FC00000ull << 32) | 0x7FC00000ull;
-  __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-__device__ __forceinline__ void publish(uint32_t *at, float h) {
-  uint32_t w = __float_as_uint(h);
-  if (w == kNoState) w = 0x7FC00000u;
-  __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// The state before chunk j (> 0) of a strip, in each lane for its channel; the lanes without
-// one (live false) only take part in the votes.  Called by one whole wave.
-template <int CH>
-__device__ __forceinline__ float state_before(const Chain &c, int64_t strip, int64_t j, int ch, bool live) {
-  const int64_t base = strip * c.chunks * CH + ch;
-  const uint64_t start = wall_clock64();
-  for (;;) {
-    uint32_t st[kWindow];
-    uint64_t pr[kWindow];
-#pragma unroll
-    for (int w = 0; w < kWindow; ++w) {
-      st[w] = 0u;
-      pr[w] = 0ull;
-      const int64_t k = j - 1 - w;
-      if (!live || k < 0) continue;
-      st[w] = __hip_atomic_load(c.states + base + k * CH, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      pr[w] = __hip_atomic_load(c.pairs + base + k * CH, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    int found = -1;
-    bool open = true;   // every pair since is there
-#pragma unroll
-    for (int w = 0; w < kWindow; ++w) {
-      if (found >= 0 || !open || j - 1 - w < 0) continue;
-      if (__all(st[w] != kNoState)) found = w;
-      else open = __all(pr[w] != kNoPair);
-    }
-    if (found >= 0) {
-      float h = 0.0f;
-#pragma unroll
-      for (int w = kWindow - 1; w >= 0; --w) {
-        if (w == found) h = __uint_as_float(st[w]);
-        else if (w < found)
-          h = apply(Pair{__uint_as_float((uint32_t)pr[w]), __uint_as_float((uint32_t)(pr[w] >> 32))}, h);
-      }
-      return h;
-    }
-    if (wall_clock64() - start > kWaitTicks) return __uint_as_float(0x7FC00000u);
-    __builtin_amdgcn_s_sleep(1);
+// Where a thread's channels are: blockIdx.x counts strips of channels, y and z step through
+// tiles and batch rows.
+template <int V>
+struct Place {
+  int64_t first, col;   // the strip's first channel, the thread's
+  int cnt;
+  __device__ __forceinline__ explicit Place(int64_t chan) {
+    first = (int64_t)blockIdx.x * (8 * V);
+    col = first + (threadIdx.x & 7) * V;
+    cnt = (int)min((int64_t)V, max((int64_t)0, chan - col));
   }
-}
-
-// Clears the chain's words before a launch that uses them.
-__global__ __launch_bounds__(256) void scan_clear_kernel(uint4 *p, int64_t n, uint32_t *ticket) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
-    p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0u;
-}
+};
 
 // What the threads of a tile share.
 template <int CH>
@@ -200,55 +154,38 @@ struct Shared {
   Pair group[kGroups][CH];     // a group's pair, then that of its segment's groups before it
   Pair seg[kSegs][CH];
   float first[kSegs][CH];      // the state before a segment
-  uint32_t tile;
 };
 
-// From every thread's pair (for its V channels) to the state before its steps.  Two barriers
-// between the pairs and the wait for the chain, one after it.
+// The threads' pairs (one per channel) into segments' pairs; each group's place then holds
+// the pair of its segment's groups before it.
 template <int V, int CH>
-__device__ __forceinline__ void states_of_groups(Shared<CH> &sh, const Chain &c, int64_t strip, int64_t j,
-                                                 int64_t c0, int64_t chan, const float *h0,
-                                                 float *h_last, const Pair (&p)[V], float (&h)[V]) {
+__device__ __forceinline__ void compose(Shared<CH> &sh, const Pair (&p)[V]) {
   const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7;
 #pragma unroll
   for (int i = 0; i < V; ++i) sh.group[group][lane * V + i] = p[i];
   __syncthreads();
   const int ch = tid % CH, seg = tid / CH;
-  {
-    Pair run = {1.0f, 0.0f};
+  Pair run = {1.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < Shared<CH>::kPer; ++i) {
-      const Pair q = sh.group[seg * Shared<CH>::kPer + i][ch];
-      sh.group[seg * Shared<CH>::kPer + i][ch] = run;
-      run = then(run, q);
-    }
-    sh.seg[seg][ch] = run;
+  for (int i = 0; i < Shared<CH>::kPer; ++i) {
+    const Pair q = sh.group[seg * Shared<CH>::kPer + i][ch];
+    sh.group[seg * Shared<CH>::kPer + i][ch] = run;
+    run = then(run, q);
   }
+  sh.seg[seg][ch] = run;
   __syncthreads();
-  if (tid < 64) {
-    const bool live = tid < CH && c0 + ch < chan;
-    Pair all = sh.seg[0][ch];
+}
+
+// The state before each thread's steps from the one before the tile; `before` (per channel,
+// read by the first CH threads) and compose()'s result.
+template <int V, int CH>
+__device__ __forceinline__ void states_of_groups(Shared<CH> &sh, float before, float (&h)[V]) {
+  const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7;
+  if (tid < CH) {
 #pragma unroll
-    for (int s = 1; s < Shared<CH>::kSegs; ++s) all = then(all, sh.seg[s][ch]);
-    const int64_t at = (strip * c.chunks + j) * CH + ch;
-    float before = 0.0f;
-    if (j == 0) {
-      if (h0 && live) before = h0[strip / c.chan_strips * chan + c0 + ch];
-    } else {
-      if (live && j + 1 < c.chunks) publish(c.pairs + at, all);
-      before = state_before<CH>(c, strip, j, ch, live);
-    }
-    const float after = apply(all, before);
-    if (live) {
-      if (j + 1 < c.chunks) publish(c.states + at, after);
-      else if (h_last) h_last[strip / c.chan_strips * chan + c0 + ch] = after;
-    }
-    if (tid < CH) {
-#pragma unroll
-      for (int s = 0; s < Shared<CH>::kSegs; ++s) {
-        sh.first[s][ch] = before;
-        before = apply(sh.seg[s][ch], before);
-      }
+    for (int s = 0; s < Shared<CH>::kSegs; ++s) {
+      sh.first[s][tid] = before;
+      before = apply(sh.seg[s][tid], before);
     }
   }
   __syncthreads();
@@ -257,80 +194,115 @@ __device__ __forceinline__ void states_of_groups(Shared<CH> &sh, const Chain &c,
     h[i] = apply(sh.group[group][lane * V + i], sh.first[group / Shared<CH>::kPer][lane * V + i]);
 }
 
-// The next tile of this workgroup: from the counter, or in strides where no tile waits.
+// The tile's pair, from the first kernel to the second.
 template <int CH>
-__device__ __forceinline__ int64_t next_tile(Shared<CH> &sh, const Chain &c, int64_t turn) {
-  if (c.chunks == 1) return (int64_t)blockIdx.x + turn * gridDim.x;
-  __syncthreads();   // the tile before is done with the shared words
-  if (threadIdx.x == 0)
-    sh.tile = __hip_atomic_fetch_add(c.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return sh.tile;
+__device__ __forceinline__ void leave_pair(Shared<CH> &sh, const Tiling &t, int64_t batch, int64_t j,
+                                           int64_t first, int64_t chan) {
+  if (threadIdx.x < CH && first + threadIdx.x < chan) {
+    Pair all = sh.seg[0][threadIdx.x];
+#pragma unroll
+    for (int s = 1; s < Shared<CH>::kSegs; ++s) all = then(all, sh.seg[s][threadIdx.x]);
+    t.pairs[(batch * t.chunks + j) * chan + first + threadIdx.x] = all;
+  }
+}
+
+// The state before a tile: the second kernel's, or where there is one tile the given one.
+template <int CH>
+__device__ __forceinline__ float state_before_tile(const Tiling &t, const float *given, int64_t batch,
+                                                   int64_t j, int64_t first, int64_t chan) {
+  if (threadIdx.x >= CH || first + threadIdx.x >= chan) return 0.0f;
+  if (j > 0) return t.states[(batch * t.chunks + j) * chan + first + threadIdx.x];
+  return given ? given[batch * chan + first + threadIdx.x] : 0.0f;
+}
+
+// The second kernel: a thread per batch row and channel walks over the tiles.
+__global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *given, int64_t chan,
+                                                         int64_t threads) {
+  for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
+    const int64_t base = i / chan * t.chunks * chan + i % chan;
+    float h = given ? given[i] : 0.0f;
+    for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += 16) {
+      Pair p[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (j0 + k + 1 < t.chunks) p[k] = t.pairs[base + (j0 + k) * chan];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if (j0 + k + 1 >= t.chunks) continue;
+        h = apply(p[k], h);
+        t.states[base + (j0 + k + 1) * chan] = h;
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- forward
-template <bool F32, bool RESET>
-__global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Chain c) {
+// PAIRS: the first kernel (all tiles but the last); otherwise the third.
+template <bool F32, bool RESET, bool PAIRS>
+__global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   __shared__ Shared<CH> sh;
-  const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
-  for (int64_t turn = 0;; ++turn) {
-    const int64_t tile = next_tile(sh, c, turn);
-    if (tile >= c.tiles) return;
-    const int64_t strip = tile % c.strips, j = tile / c.strips;
-    const int64_t batch = strip / c.chan_strips, c0 = strip % c.chan_strips * CH, col = c0 + lane * V;
-    const int cnt = (int)min((int64_t)V, max((int64_t)0, a.chan - col));
-    const int64_t t0 = j * kTile + group * kSteps;
-    Raw<F32> g[kSteps], u[kSteps];
+  const Place<V> at(a.chan);
+  const int group = threadIdx.x >> 3;
+  float fl[V];
+  load_f32<V>(a.floor, at.col, at.cnt, fl);
+  for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
+    for (int64_t j = blockIdx.y; j < tl.chunks - PAIRS; j += gridDim.y) {
+      const int64_t t0 = j * kTile + group * kSteps;
+      Raw<F32> g[kSteps], u[kSteps];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      g[s].zero();
-      u[s].zero();
-      if (t0 + s >= a.time) continue;
-      g[s].load(a.g, batch * a.g_batch + (t0 + s) * a.g_time + col, cnt);
-      u[s].load(a.u, batch * a.u_batch + (t0 + s) * a.u_time + col, cnt);
-    }
-    float fl[V];
-    load_f32<V>(a.floor, col, cnt, fl);
-    float av[kSteps][V], bv[kSteps][V];
-    Pair p[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const bool in = t0 + s < a.time;
-      const bool cut = RESET && in && a.reset[batch * a.time + t0 + s];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float sg, sc;
-        sigmoids(g[s].get(i), sg, sc);
-        const float uv = u[s].get(i), rest = 1.0f - fl[i];
-        float x = __builtin_fmaf(rest, sg, fl[i]), y = rest * sc * uv;
-        if (RESET && cut) {
-          x = cut_mark();
-          y = uv;
-        }
-        if (!in) {        // past the end: the state stays
-          x = 1.0f;
-          y = 0.0f;
-        }
-        av[s][i] = x;
-        bv[s][i] = y;
-        p[i] = RESET ? then(p[i], Pair{x, y}) : Pair{x * p[i].a, __builtin_fmaf(x, p[i].b, y)};
+      for (int s = 0; s < kSteps; ++s) {
+        g[s].zero();
+        u[s].zero();
+        if (!PAIRS && t0 + s >= a.time) continue;
+        g[s].load(a.g, batch * a.g_batch + (t0 + s) * a.g_time + at.col, at.cnt);
+        u[s].load(a.u, batch * a.u_batch + (t0 + s) * a.u_time + at.col, at.cnt);
       }
-    }
-    float h[V];
-    states_of_groups<V, CH>(sh, c, strip, j, c0, a.chan, a.h0, a.h_last, p, h);
+      const float before = PAIRS ? 0.0f : state_before_tile<CH>(tl, a.h0, batch, j, at.first, a.chan);
+      float av[kSteps][V], bv[kSteps][V];
+      Pair p[V];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (t0 + s >= a.time) break;
+      for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
+      bool cut[kSteps];
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        h[i] = RESET ? apply(Pair{av[s][i], bv[s][i]}, h[i]) : __builtin_fmaf(av[s][i], h[i], bv[s][i]);
-      store<F32>(a.y, batch * a.y_batch + (t0 + s) * a.y_time + col, cnt, h);
+      for (int s = 0; s < kSteps; ++s) {
+        // (steps past the end, all in the last tile, lead nowhere)
+        cut[s] = RESET && (PAIRS || t0 + s < a.time) && a.reset[batch * a.time + t0 + s];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float sg, sc;
+          sigmoids(g[s].get(i), sg, sc);
+          const float uv = u[s].get(i), rest = 1.0f - fl[i];
+          av[s][i] = __builtin_fmaf(rest, sg, fl[i]);
+          bv[s][i] = rest * sc * uv;
+          if (RESET && cut[s]) bv[s][i] = uv;
+          p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
+          if (RESET && cut[s]) p[i] = Pair{cut_mark(), bv[s][i]};
+        }
+      }
+      compose<V, CH>(sh, p);
+      if constexpr (PAIRS) {
+        leave_pair<CH>(sh, tl, batch, j, at.first, a.chan);
+      } else {
+        float h[V];
+        states_of_groups<V, CH>(sh, before, h);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          if (t0 + s >= a.time) break;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
+            if (RESET && cut[s]) h[i] = bv[s][i];
+          }
+          store<F32>(a.y, batch * a.y_batch + (t0 + s) * a.y_time + at.col, at.cnt, h);
+          if (t0 + s == a.time - 1 && a.h_last)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (i < at.cnt) a.h_last[batch * a.chan + at.col + i] = h[i];
+        }
+      }
+      __syncthreads();   // before the next tile writes the shared words
     }
-    if (c.chunks == 1) __syncthreads();   // before the next tile writes the shared words
-  }
 }
 
 // A thread per V channels walks over the steps.
@@ -403,86 +375,104 @@ __device__ __forceinline__ void state_before_step(const nvfp4_scan_args &a, int6
 }
 
 // Time runs backward: a thread's step s is t = time - 1 - (j kTile + group kSteps + s).
-template <bool F32, bool RESET>
-__global__ __launch_bounds__(256) void scan_backward_kernel(ScanLaunch l, Chain c, float *floors) {
+// PAIRS: the first kernel, of the carries c -> a (c + dy), from g and dy; otherwise the third.
+template <bool F32, bool RESET, bool PAIRS>
+__global__ __launch_bounds__(256) void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   __shared__ Shared<CH> sh;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
+  const Place<V> at(a.chan);
   const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
-  for (int64_t turn = 0;; ++turn) {
-    const int64_t tile = next_tile(sh, c, turn);
-    if (tile >= c.tiles) return;
-    const int64_t strip = tile % c.strips, j = tile / c.strips;
-    const int64_t batch = strip / c.chan_strips, c0 = strip % c.chan_strips * CH, col = c0 + lane * V;
-    const int cnt = (int)min((int64_t)V, max((int64_t)0, a.chan - col));
-    const int64_t last = a.time - 1 - (j * kTile + group * kSteps);   // of the thread's steps
-    Raw<F32> g[kSteps], u[kSteps], dy[kSteps], y[kSteps];
+  float fl[V];
+  load_f32<V>(a.floor, at.col, at.cnt, fl);
+  for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
+    for (int64_t j = blockIdx.y; j < tl.chunks - PAIRS; j += gridDim.y) {
+      const int64_t last = a.time - 1 - (j * kTile + group * kSteps);   // of the thread's steps
+      Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      g[s].zero(); u[s].zero(); dy[s].zero(); y[s].zero();
-      const int64_t t = last - s;
-      if (t < 0) continue;
-      g[s].load(a.g, batch * a.g_batch + t * a.g_time + col, cnt);
-      dy[s].load(d.dy, batch * d.dy_batch + t * d.dy_time + col, cnt);
-      u[s].load(a.u, batch * a.u_batch + t * a.u_time + col, cnt);
-      if (t > 0) y[s].load(a.y, batch * a.y_batch + (t - 1) * a.y_time + col, cnt);
-    }
-    float fl[V];
-    load_f32<V>(a.floor, col, cnt, fl);
-    Pair p[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
-    bool cut[kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const bool in = last - s >= 0;
-      cut[s] = RESET && in && a.reset[batch * a.time + last - s];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float sg, sc;
-        sigmoids(g[s].get(i), sg, sc);
-        const float x = in ? __builtin_fmaf(1.0f - fl[i], sg, fl[i]) : 1.0f;
-        if (RESET && cut[s]) p[i] = Pair{cut_mark(), 0.0f};
-        else p[i] = Pair{is_cut(p[i].a) ? p[i].a : x * p[i].a, x * (p[i].b + dy[s].get(i))};
+      for (int s = 0; s < kSteps; ++s) {
+        g[s].zero();
+        dy[s].zero();
+        const int64_t t = last - s;
+        if (!PAIRS && t < 0) continue;
+        g[s].load(a.g, batch * a.g_batch + t * a.g_time + at.col, at.cnt);
+        dy[s].load(d.dy, batch * d.dy_batch + t * d.dy_time + at.col, at.cnt);
       }
-    }
-    float h[V], dfl[V];
-    states_of_groups<V, CH>(sh, c, strip, j, c0, a.chan, d.dh_last, d.dh0, p, h);
+      if (!PAIRS) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int64_t t = last - s;
-      if (t < 0) break;
-      float before[V], dg[V], du[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) before[i] = y[s].get(i);
-      if (t == 0) load_f32<V>(a.h0, batch * a.chan + col, cnt, before);
-      backward_step<F32>(g[s], u[s], dy[s], before, RESET && cut[s], fl, h, dg, du, dfl);
-      store<F32>(d.dg, batch * d.dg_batch + t * d.dg_time + col, cnt, dg);
-      store<F32>(d.du, batch * d.du_batch + t * d.du_time + col, cnt, du);
-    }
-    if (d.dfloor) {   // the tile's sum over its steps, per channel
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < V; ++i) sh.group[group][lane * V + i].a = dfl[i];
-      __syncthreads();
-      const int ch = threadIdx.x % CH, seg = threadIdx.x / CH;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
-      sh.first[seg][ch] = sum;
-      __syncthreads();
-      if (threadIdx.x < CH && c0 + ch < a.chan) {
-        sum = 0.0f;
-#pragma unroll
-        for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
-        floors[(batch * c.chunks + j) * a.chan + c0 + ch] = sum;
+        for (int s = 0; s < kSteps; ++s) {
+          u[s].zero();
+          y[s].zero();
+          const int64_t t = last - s;
+          if (t < 0) continue;
+          u[s].load(a.u, batch * a.u_batch + t * a.u_time + at.col, at.cnt);
+          if (t > 0) y[s].load(a.y, batch * a.y_batch + (t - 1) * a.y_time + at.col, at.cnt);
+        }
       }
+      const float before = PAIRS ? 0.0f : state_before_tile<CH>(tl, d.dh_last, batch, j, at.first, a.chan);
+      Pair p[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
+      bool cut[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        // (steps before the beginning, all in the last tile, lead nowhere)
+        cut[s] = RESET && (PAIRS || last - s >= 0) && a.reset[batch * a.time + last - s];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float sg, sc;
+          sigmoids(g[s].get(i), sg, sc);
+          const float x = __builtin_fmaf(1.0f - fl[i], sg, fl[i]);
+          p[i] = Pair{x * p[i].a, x * (p[i].b + dy[s].get(i))};
+          if (RESET && cut[s]) p[i] = Pair{cut_mark(), 0.0f};
+        }
+      }
+      compose<V, CH>(sh, p);
+      if constexpr (PAIRS) {
+        leave_pair<CH>(sh, tl, batch, j, at.first, a.chan);
+      } else {
+        float c[V], dfl[V];
+        states_of_groups<V, CH>(sh, before, c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const int64_t t = last - s;
+          if (t < 0) break;
+          float prior[V], dg[V], du[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) prior[i] = y[s].get(i);
+          if (t == 0) load_f32<V>(a.h0, batch * a.chan + at.col, at.cnt, prior);
+          backward_step<F32>(g[s], u[s], dy[s], prior, RESET && cut[s], fl, c, dg, du, dfl);
+          store<F32>(d.dg, batch * d.dg_batch + t * d.dg_time + at.col, at.cnt, dg);
+          store<F32>(d.du, batch * d.du_batch + t * d.du_time + at.col, at.cnt, du);
+          if (t == 0 && d.dh0)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (i < at.cnt) d.dh0[batch * a.chan + at.col + i] = c[i];
+        }
+        if (d.dfloor) {   // the tile's sum over its steps, per channel
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < V; ++i) sh.group[group][lane * V + i].a = dfl[i];
+          __syncthreads();
+          const int ch = threadIdx.x % CH, seg = threadIdx.x / CH;
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
+          sh.first[seg][ch] = sum;
+          __syncthreads();
+          if (threadIdx.x < CH && at.first + ch < a.chan) {
+            sum = 0.0f;
+#pragma unroll
+            for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
+            floors[(batch * tl.chunks + j) * a.chan + at.first + ch] = sum;
+          }
+        }
+      }
+      __syncthreads();   // before the next tile writes the shared words
     }
-    if (c.chunks == 1) __syncthreads();   // before the next tile writes the shared words
-  }
 }
 
 template <bool F32>
@@ -541,40 +531,66 @@ __global__ __launch_bounds__(1024) void scan_floor_kernel(const float *sums, int
 // ---------------------------------------------------------------- launches
 constexpr int kCus = 256;
 
-// Workspace: the ticket and the chain's words (more than one chunk), then the tiles' sums
-// for dfloor (backward).
+// Workspace: the tiles' pairs and states (more than one tile), then their sums for dfloor
+// (backward).
 struct Layout {
-  Chain c;
-  size_t words;     // bytes to clear, after the ticket's 16
-  size_t floors;    // offset of the sums
-  size_t bytes;
+  int64_t chunks;
+  size_t states, floors, bytes;   // offsets, and the whole
 };
 
-Layout layout_of(int64_t batch, int64_t time, int64_t chan, bool f32, bool backward) {
-  const int64_t ch = f32 ? 32 : 64;
+Layout layout_of(int64_t batch, int64_t time, int64_t chan, bool backward) {
   Layout l;
-  l.c.chan_strips = (chan + ch - 1) / ch;
-  l.c.strips = batch * l.c.chan_strips;
-  l.c.chunks = time <= kShort ? 1 : (time + kTile - 1) / kTile;
-  l.c.tiles = l.c.strips * l.c.chunks;
-  l.words = l.c.chunks > 1 ? (size_t)l.c.tiles * ch * 12 : 0;
-  l.floors = l.words ? 16 + ((l.words + 15) & ~(size_t)15) : 0;
-  l.bytes = l.floors + (backward ? 4 * (size_t)(batch * l.c.chunks * chan) : 0);
+  l.chunks = time <= kShort ? 1 : (time + kTile - 1) / kTile;
+  const size_t n = (size_t)(batch * l.chunks * chan), tiled = l.chunks > 1 ? n : 0;
+  l.states = 8 * tiled;
+  l.floors = 12 * tiled;
+  l.bytes = l.floors + (backward ? 4 * n : 0);
   return l;
 }
 
-uint32_t grid_of(int64_t wgs, int64_t most) { return (uint32_t)(wgs < most ? wgs : most); }
-
-// Clears the chain's words where there is a chain.
-hipError_t prepare_chain(Layout &l, void *ws, hipStream_t stream) {
-  if (!l.words) return hipSuccess;
+Tiling tiling_of(const Layout &l, void *ws) {
   char *p = static_cast<char *>(ws);
-  l.c.ticket = reinterpret_cast<uint32_t *>(p);
-  l.c.pairs = reinterpret_cast<uint64_t *>(p + 16);
-  l.c.states = reinterpret_cast<uint32_t *>(p + 16 + l.words / 12 * 8);
-  const int64_t n = (int64_t)((l.words + 15) / 16);
-  scan_clear_kernel<<<grid_of((n + 255) / 256, 4 * kCus), 256, 0, stream>>>(
-      reinterpret_cast<uint4 *>(p + 16), n, l.c.ticket);
+  return Tiling{l.chunks, reinterpret_cast<Pair *>(p), reinterpret_cast<float *>(p + l.states)};
+}
+
+uint32_t at_most(int64_t n, int64_t most) { return (uint32_t)(n < most ? n : most); }
+
+// (Channels beyond 2^31 are refused before; the other two step.)
+dim3 tile_grid(const nvfp4_scan_args &a, int64_t chunks, int ch) {
+  return dim3((uint32_t)((a.chan + ch - 1) / ch), at_most(chunks, 65535), at_most(a.batch, 65535));
+}
+
+hipError_t launch_states(const nvfp4_scan_args &a, const Tiling &t, const float *given, hipStream_t stream) {
+  const int64_t threads = a.batch * a.chan;
+  scan_states_kernel<<<at_most((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(t, given, a.chan, threads);
+  return hipGetLastError();
+}
+
+template <bool F32, bool RESET>
+hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
+  const Tiling t = tiling_of(l, s.ws);
+  const int ch = 8 * Raw<F32>::V;
+  hipError_t e;
+  if (l.chunks > 1) {
+    scan_forward_kernel<F32, RESET, true><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s.a, t);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_states(s.a, t, s.a.h0, stream)) != hipSuccess) return e;
+  }
+  scan_forward_kernel<F32, RESET, false><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s.a, t);
+  return hipGetLastError();
+}
+
+template <bool F32, bool RESET>
+hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
+  const Tiling t = tiling_of(l, s.ws);
+  const int ch = 8 * Raw<F32>::V;
+  hipError_t e;
+  if (l.chunks > 1) {
+    scan_backward_kernel<F32, RESET, true><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s, t, floors);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_states(s.a, t, s.d.dh_last, stream)) != hipSuccess) return e;
+  }
+  scan_backward_kernel<F32, RESET, false><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s, t, floors);
   return hipGetLastError();
 }
 
@@ -583,39 +599,33 @@ hipError_t run_forward(const ScanLaunch &s, hipStream_t stream) {
   const nvfp4_scan_args &a = s.a;
   if (a.time <= kShort) {
     const int64_t threads = a.batch * ((a.chan + Raw<F32>::V - 1) / Raw<F32>::V);
-    scan_forward_short_kernel<F32><<<grid_of((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(a, threads);
+    scan_forward_short_kernel<F32><<<at_most((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(a, threads);
     return hipGetLastError();
   }
-  Layout l = layout_of(a.batch, a.time, a.chan, F32, false);
-  const hipError_t e = prepare_chain(l, s.ws, stream);
-  if (e != hipSuccess) return e;
-  const uint32_t grid = grid_of(l.c.tiles, 8 * kCus);
-  if (a.reset) scan_forward_kernel<F32, true><<<grid, 256, 0, stream>>>(a, l.c);
-  else scan_forward_kernel<F32, false><<<grid, 256, 0, stream>>>(a, l.c);
-  return hipGetLastError();
+  const Layout l = layout_of(a.batch, a.time, a.chan, false);
+  return a.reset ? forward_tiles<F32, true>(s, l, stream) : forward_tiles<F32, false>(s, l, stream);
 }
 
 template <bool F32>
 hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
   const nvfp4_scan_args &a = s.a;
-  Layout l = layout_of(a.batch, a.time, a.chan, F32, true);
+  const Layout l = layout_of(a.batch, a.time, a.chan, true);
   float *floors = reinterpret_cast<float *>(static_cast<char *>(s.ws) + l.floors);
   hipError_t e = hipSuccess;
   if (a.batch > 0) {
     if (a.time <= kShort) {
       const int64_t threads = a.batch * ((a.chan + Raw<F32>::V - 1) / Raw<F32>::V);
-      scan_backward_short_kernel<F32><<<grid_of((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(
+      scan_backward_short_kernel<F32><<<at_most((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(
           s, threads, a.time && s.d.dfloor ? floors : nullptr);   // (no steps: no workspace)
+      e = hipGetLastError();
     } else {
-      if ((e = prepare_chain(l, s.ws, stream)) != hipSuccess) return e;
-      const uint32_t grid = grid_of(l.c.tiles, 8 * kCus);
-      if (a.reset) scan_backward_kernel<F32, true><<<grid, 256, 0, stream>>>(s, l.c, floors);
-      else scan_backward_kernel<F32, false><<<grid, 256, 0, stream>>>(s, l.c, floors);
+      e = a.reset ? backward_tiles<F32, true>(s, l, floors, stream)
+                  : backward_tiles<F32, false>(s, l, floors, stream);
     }
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (e != hipSuccess) return e;
   }
   if (!s.d.dfloor) return e;
-  const int64_t rows = a.time ? a.batch * l.c.chunks : 0;
+  const int64_t rows = a.time ? a.batch * l.chunks : 0;
   scan_floor_kernel<<<(uint32_t)((a.chan + 31) / 32), 1024, 0, stream>>>(floors, rows, a.chan, s.d.dfloor);
   return hipGetLastError();
 }
@@ -623,11 +633,7 @@ hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t batch, int64_t time, int64_t chan, bool backward) {
-  // the larger of the two types' (binary32 strips are half as wide: their last one may
-  // have fewer unused channels)
-  const size_t a = layout_of(batch, time, chan, false, backward).bytes;
-  const size_t b = layout_of(batch, time, chan, true, backward).bytes;
-  return a > b ? a : b;
+  return layout_of(batch, time, chan, backward).bytes;
 }
 
 hipError_t launch_scan_forward(const ScanLaunch &s, hipStream_t stream) {
