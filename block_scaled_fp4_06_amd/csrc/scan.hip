@@ -36,7 +36,9 @@ constexpr int kShort = 16;           // steps that one thread walks over by itse
 
 // ---------------------------------------------------------------- loads and stores
 // 16 bytes of channels, at any element's alignment (the packed type makes them single
-// instructions); `cnt` of them exist.
+// instructions).  PART: only `cnt` of the elements exist (fewer channels than one access
+// covers); otherwise a strip's last lanes take the last whole access, so that no load
+// depends on a branch, and store their own channels alone.
 struct __attribute__((packed, aligned(2))) Four { uint32_t w[4]; };
 
 template <bool F32>
@@ -44,18 +46,19 @@ struct Raw {
   static constexpr int V = F32 ? 4 : 8;
   uint32_t w[4];
 
-  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
-  __device__ __forceinline__ void load(const void *p, int64_t i, int cnt) {
-    if (cnt >= V) {
-      const Four v = *reinterpret_cast<const Four *>(static_cast<const char *>(p) + i * (F32 ? 4 : 2));
+  template <bool PART>
+  __device__ __forceinline__ void load(const char *p, int cnt) {
+    if constexpr (!PART) {
+      const Four v = *reinterpret_cast<const Four *>(p);
 #pragma unroll
       for (int l = 0; l < 4; ++l) w[l] = v.w[l];
     } else {
+      w[0] = w[1] = w[2] = w[3] = 0u;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if (j >= cnt) continue;
-        if constexpr (F32) w[j] = static_cast<const uint32_t *>(p)[i + j];
-        else w[j >> 1] |= (uint32_t) static_cast<const uint16_t *>(p)[i + j] << (16 * (j & 1));
+        if constexpr (F32) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+        else w[j >> 1] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
       }
     }
   }
@@ -65,41 +68,45 @@ struct Raw {
   }
 };
 
+// Two bf16 values in a word, nearest-even.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef __bf16 Two __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, Two{(__bf16)lo, (__bf16)hi});
+}
+
+// Elements from .. to - 1 of the V at p.
 template <bool F32>
-__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const float (&v)[F32 ? 4 : 8]) {
-  if (cnt >= (F32 ? 4 : 8)) {
+__device__ __forceinline__ void store(char *p, int from, int to, const float (&v)[F32 ? 4 : 8]) {
+  constexpr int V = F32 ? 4 : 8;
+  if (from <= 0 && to >= V) {
     Four f;
 #pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      if constexpr (F32) f.w[l] = __float_as_uint(v[l]);
-      else f.w[l] = (uint32_t)bf16_bits_rn(v[2 * l]) | ((uint32_t)bf16_bits_rn(v[2 * l + 1]) << 16);
-    }
-    *reinterpret_cast<Four *>(static_cast<char *>(p) + i * (F32 ? 4 : 2)) = f;
+    for (int l = 0; l < 4; ++l) f.w[l] = F32 ? __float_as_uint(v[l & 3]) : pack2(v[(2 * l) % V], v[(2 * l + 1) % V]);
+    *reinterpret_cast<Four *>(p) = f;
   } else {
 #pragma unroll
-    for (int j = 0; j < (F32 ? 4 : 8); ++j) {
-      if (j >= cnt) continue;
-      if constexpr (F32) static_cast<float *>(p)[i + j] = v[j];
-      else static_cast<uint16_t *>(p)[i + j] = bf16_bits_rn(v[j]);
+    for (int j = 0; j < V; ++j) {
+      if (j < from || j >= to) continue;
+      if constexpr (F32) reinterpret_cast<float *>(p)[j] = v[j];
+      else reinterpret_cast<uint16_t *>(p)[j] = bf16_bits_rn(v[j]);
     }
   }
 }
 
+template <bool F32>
+__device__ __forceinline__ const char *at(const void *p, int64_t i) {
+  return static_cast<const char *>(p) + i * (F32 ? 4 : 2);
+}
+template <bool F32>
+__device__ __forceinline__ char *at(void *p, int64_t i) {
+  return static_cast<char *>(p) + i * (F32 ? 4 : 2);
+}
+
 // V binary32 values (floor, states); zero where there are none.
-template <int V>
+template <int V, bool PART>
 __device__ __forceinline__ void load_f32(const float *p, int64_t i, int cnt, float (&v)[V]) {
-  if (p && cnt >= V) {
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      Raw<true> r;
-      r.load(p, i + j, 4);
-#pragma unroll
-      for (int l = 0; l < 4; ++l) v[j + l] = r.get(l);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = p && j < cnt ? p[i + j] : 0.0f;
-  }
+  for (int j = 0; j < V; ++j) v[j] = p && (!PART || j < cnt) ? p[i + j] : 0.0f;
 }
 
 // ---------------------------------------------------------------- arithmetic
@@ -134,18 +141,40 @@ struct Tiling {
   float *states;      // [batch][chunk][channel]
 };
 
-// Where a thread's channels are: blockIdx.x counts strips of channels, y and z step through
-// tiles and batch rows.
-template <int V>
+// Where a thread's V channels are: blockIdx.x counts strips of 8 V.  Its own are the
+// elements own .. cnt - 1 of the access at col.
+template <int V, bool PART>
 struct Place {
-  int64_t first, col;   // the strip's first channel, the thread's
-  int cnt;
+  int64_t first, col;   // the strip's first channel; the thread's access
+  int own, cnt;
   __device__ __forceinline__ explicit Place(int64_t chan) {
     first = (int64_t)blockIdx.x * (8 * V);
     col = first + (threadIdx.x & 7) * V;
-    cnt = (int)min((int64_t)V, max((int64_t)0, chan - col));
+    own = 0;
+    cnt = V;
+    if constexpr (PART) {
+      cnt = (int)min((int64_t)V, max((int64_t)0, chan - col));
+    } else if (col > chan - V) {   // (chan >= V)
+      own = (int)min((int64_t)V, col - (chan - V));
+      col = chan - V;
+    }
   }
 };
+
+// The channel that thread tid < 8 V of a tile looks after between the kernels (that of
+// element tid % V of lane tid / V), and whether it is that lane's own.
+template <int V, bool PART>
+__device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t chan, bool &own) {
+  const int64_t c = first + tid;
+  if constexpr (PART) {
+    own = c < chan;
+    return c;
+  } else {
+    const int64_t lane = first + tid / V * V, moved = max((int64_t)0, lane - (chan - V));
+    own = tid % V >= moved;
+    return c - moved;
+  }
+}
 
 // What the threads of a tile share.
 template <int CH>
@@ -195,24 +224,28 @@ __device__ __forceinline__ void states_of_groups(Shared<CH> &sh, float before, f
 }
 
 // The tile's pair, from the first kernel to the second.
-template <int CH>
-__device__ __forceinline__ void leave_pair(Shared<CH> &sh, const Tiling &t, int64_t batch, int64_t j,
+template <int V, bool PART>
+__device__ __forceinline__ void leave_pair(Shared<8 * V> &sh, const Tiling &t, int64_t batch, int64_t j,
                                            int64_t first, int64_t chan) {
-  if (threadIdx.x < CH && first + threadIdx.x < chan) {
-    Pair all = sh.seg[0][threadIdx.x];
+  if (threadIdx.x >= 8 * V) return;
+  bool own;
+  const int64_t c = channel_of<V, PART>(threadIdx.x, first, chan, own);
+  Pair all = sh.seg[0][threadIdx.x];
 #pragma unroll
-    for (int s = 1; s < Shared<CH>::kSegs; ++s) all = then(all, sh.seg[s][threadIdx.x]);
-    t.pairs[(batch * t.chunks + j) * chan + first + threadIdx.x] = all;
-  }
+  for (int s = 1; s < Shared<8 * V>::kSegs; ++s) all = then(all, sh.seg[s][threadIdx.x]);
+  if (own) t.pairs[(batch * t.chunks + j) * chan + c] = all;
 }
 
-// The state before a tile: the second kernel's, or where there is one tile the given one.
-template <int CH>
+// The state before a tile: the second kernel's, or before the first tile the given one.
+template <int V, bool PART>
 __device__ __forceinline__ float state_before_tile(const Tiling &t, const float *given, int64_t batch,
                                                    int64_t j, int64_t first, int64_t chan) {
-  if (threadIdx.x >= CH || first + threadIdx.x >= chan) return 0.0f;
-  if (j > 0) return t.states[(batch * t.chunks + j) * chan + first + threadIdx.x];
-  return given ? given[batch * chan + first + threadIdx.x] : 0.0f;
+  if (threadIdx.x >= 8 * V) return 0.0f;
+  bool own;
+  const int64_t c = channel_of<V, PART>(threadIdx.x, first, chan, own);
+  if (PART && !own) return 0.0f;
+  if (j > 0) return t.states[(batch * t.chunks + j) * chan + c];
+  return given ? given[batch * chan + c] : 0.0f;
 }
 
 // The second kernel: a thread per batch row and channel walks over the tiles.
@@ -237,28 +270,30 @@ __global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *
 }
 
 // ---------------------------------------------------------------- forward
-// PAIRS: the first kernel (all tiles but the last); otherwise the third.
-template <bool F32, bool RESET, bool PAIRS>
+// PAIRS: the first kernel (all tiles but the last); otherwise the third.  Steps past the end
+// (all in the last tile) read the last one again and lead nowhere.
+template <bool F32, bool RESET, bool PAIRS, bool PART>
 __global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   __shared__ Shared<CH> sh;
-  const Place<V> at(a.chan);
+  const Place<V, PART> pl(a.chan);
   const int group = threadIdx.x >> 3;
   float fl[V];
-  load_f32<V>(a.floor, at.col, at.cnt, fl);
+  load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
   for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
     for (int64_t j = blockIdx.y; j < tl.chunks - PAIRS; j += gridDim.y) {
-      const int64_t t0 = j * kTile + group * kSteps;
+      const int64_t t0 = min(j * kTile + group * kSteps, a.time - 1);
+      const int more = (int)min((int64_t)kSteps, a.time - (j * kTile + group * kSteps));   // steps there are
+      const int last = max(0, more - 1);
+      const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
+      const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
       Raw<F32> g[kSteps], u[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        g[s].zero();
-        u[s].zero();
-        if (!PAIRS && t0 + s >= a.time) continue;
-        g[s].load(a.g, batch * a.g_batch + (t0 + s) * a.g_time + at.col, at.cnt);
-        u[s].load(a.u, batch * a.u_batch + (t0 + s) * a.u_time + at.col, at.cnt);
+        g[s].template load<PART>(at<F32>(pg, min(s, last) * a.g_time), pl.cnt);
+        u[s].template load<PART>(at<F32>(pu, min(s, last) * a.u_time), pl.cnt);
       }
-      const float before = PAIRS ? 0.0f : state_before_tile<CH>(tl, a.h0, batch, j, at.first, a.chan);
+      const float before = PAIRS ? 0.0f : state_before_tile<V, PART>(tl, a.h0, batch, j, pl.first, a.chan);
       float av[kSteps][V], bv[kSteps][V];
       Pair p[V];
 #pragma unroll
@@ -266,8 +301,7 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Ti
       bool cut[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        // (steps past the end, all in the last tile, lead nowhere)
-        cut[s] = RESET && (PAIRS || t0 + s < a.time) && a.reset[batch * a.time + t0 + s];
+        cut[s] = RESET && a.reset[batch * a.time + t0 + min(s, last)];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           float sg, sc;
@@ -282,55 +316,54 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Ti
       }
       compose<V, CH>(sh, p);
       if constexpr (PAIRS) {
-        leave_pair<CH>(sh, tl, batch, j, at.first, a.chan);
+        leave_pair<V, PART>(sh, tl, batch, j, pl.first, a.chan);
       } else {
         float h[V];
         states_of_groups<V, CH>(sh, before, h);
+        char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          if (t0 + s >= a.time) break;
+          if (s >= more) break;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
             if (RESET && cut[s]) h[i] = bv[s][i];
           }
-          store<F32>(a.y, batch * a.y_batch + (t0 + s) * a.y_time + at.col, at.cnt, h);
-          if (t0 + s == a.time - 1 && a.h_last)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-              if (i < at.cnt) a.h_last[batch * a.chan + at.col + i] = h[i];
+          store<F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
         }
+        if (a.h_last && j + 1 == tl.chunks && more > 0 && more <= kSteps && t0 + more == a.time)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
       }
       __syncthreads();   // before the next tile writes the shared words
     }
 }
 
-// A thread per V channels walks over the steps.
-template <bool F32>
+// A thread per V channels walks over the steps (the last thread of a row has the rest).
+template <bool F32, bool PART>
 __global__ __launch_bounds__(64) void scan_forward_short_kernel(nvfp4_scan_args a, int64_t threads) {
   constexpr int V = Raw<F32>::V;
-  const int64_t per = (a.chan + V - 1) / V;
+  const int64_t per = PART ? (a.chan + V - 1) / V : a.chan / V;
   for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
     const int64_t b = i / per, col = i % per * V;
     const int cnt = (int)min((int64_t)V, a.chan - col);
     float fl[V], h[V];
-    load_f32<V>(a.floor, col, cnt, fl);
-    load_f32<V>(a.h0, b * a.chan + col, cnt, h);
+    load_f32<V, PART>(a.floor, col, cnt, fl);
+    load_f32<V, PART>(a.h0, b * a.chan + col, cnt, h);
     for (int64_t t = 0; t < a.time; ++t) {
       Raw<F32> g, u;
-      g.zero();
-      u.zero();
-      g.load(a.g, b * a.g_batch + t * a.g_time + col, cnt);
-      u.load(a.u, b * a.u_batch + t * a.u_time + col, cnt);
+      g.template load<PART>(at<F32>(a.g, b * a.g_batch + t * a.g_time + col), cnt);
+      u.template load<PART>(at<F32>(a.u, b * a.u_batch + t * a.u_time + col), cnt);
       const bool cut = a.reset && a.reset[b * a.time + t];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         float s, sc;
         sigmoids(g.get(k), s, sc);
-        const float rest = 1.0f - fl[k];
-        h[k] = cut ? u.get(k) : (fl[k] + rest * s) * h[k] + rest * sc * u.get(k);
+        const float rest = 1.0f - fl[k], x = __builtin_fmaf(rest, s, fl[k]);
+        h[k] = cut ? u.get(k) : __builtin_fmaf(x, h[k], rest * sc * u.get(k));
       }
-      store<F32>(a.y, b * a.y_batch + t * a.y_time + col, cnt, h);
+      store<F32>(at<F32>(a.y, b * a.y_batch + t * a.y_time + col), 0, cnt, h);
     }
     if (a.h_last)
 #pragma unroll
@@ -360,65 +393,50 @@ __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> 
   }
 }
 
-template <bool F32>
-__device__ __forceinline__ void state_before_step(const nvfp4_scan_args &a, int64_t b, int64_t t, int64_t col,
-                                                  int cnt, float (&h)[Raw<F32>::V]) {
-  if (t > 0) {
-    Raw<F32> y;
-    y.zero();
-    y.load(a.y, b * a.y_batch + (t - 1) * a.y_time + col, cnt);
-#pragma unroll
-    for (int i = 0; i < Raw<F32>::V; ++i) h[i] = y.get(i);
-  } else {
-    load_f32<Raw<F32>::V>(a.h0, b * a.chan + col, cnt, h);
-  }
-}
-
 // Time runs backward: a thread's step s is t = time - 1 - (j kTile + group kSteps + s).
 // PAIRS: the first kernel, of the carries c -> a (c + dy), from g and dy; otherwise the third.
-template <bool F32, bool RESET, bool PAIRS>
-__global__ __launch_bounds__(256) void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
+// Steps before the beginning (all in the last tile) read the first one again and lead nowhere.
+template <bool F32, bool RESET, bool PAIRS, bool PART>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   __shared__ Shared<CH> sh;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
-  const Place<V> at(a.chan);
+  const Place<V, PART> pl(a.chan);
   const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
   float fl[V];
-  load_f32<V>(a.floor, at.col, at.cnt, fl);
+  load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
   for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
     for (int64_t j = blockIdx.y; j < tl.chunks - PAIRS; j += gridDim.y) {
-      const int64_t last = a.time - 1 - (j * kTile + group * kSteps);   // of the thread's steps
+      const int64_t steps = a.time - (j * kTile + group * kSteps);   // from the thread's first on
+      const int64_t t0 = max((int64_t)0, steps - 1);
+      const int more = (int)min((int64_t)kSteps, steps), last = max(0, more - 1);
+      const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
+      const char *pdy = at<F32>(d.dy, batch * d.dy_batch + t0 * d.dy_time + pl.col);
       Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        g[s].zero();
-        dy[s].zero();
-        const int64_t t = last - s;
-        if (!PAIRS && t < 0) continue;
-        g[s].load(a.g, batch * a.g_batch + t * a.g_time + at.col, at.cnt);
-        dy[s].load(d.dy, batch * d.dy_batch + t * d.dy_time + at.col, at.cnt);
+        g[s].template load<PART>(at<F32>(pg, -min(s, last) * a.g_time), pl.cnt);
+        dy[s].template load<PART>(at<F32>(pdy, -min(s, last) * d.dy_time), pl.cnt);
       }
-      if (!PAIRS) {
+      if constexpr (!PAIRS) {
+        const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
+        const char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
+        const int prior = (int)min((int64_t)kSteps, t0);   // (before the first step there is h0)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          u[s].zero();
-          y[s].zero();
-          const int64_t t = last - s;
-          if (t < 0) continue;
-          u[s].load(a.u, batch * a.u_batch + t * a.u_time + at.col, at.cnt);
-          if (t > 0) y[s].load(a.y, batch * a.y_batch + (t - 1) * a.y_time + at.col, at.cnt);
+          u[s].template load<PART>(at<F32>(pu, -min(s, last) * a.u_time), pl.cnt);
+          y[s].template load<PART>(at<F32>(py, -min(s + 1, prior) * a.y_time), pl.cnt);
         }
       }
-      const float before = PAIRS ? 0.0f : state_before_tile<CH>(tl, d.dh_last, batch, j, at.first, a.chan);
+      const float before = PAIRS ? 0.0f : state_before_tile<V, PART>(tl, d.dh_last, batch, j, pl.first, a.chan);
       Pair p[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
       bool cut[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        // (steps before the beginning, all in the last tile, lead nowhere)
-        cut[s] = RESET && (PAIRS || last - s >= 0) && a.reset[batch * a.time + last - s];
+        cut[s] = RESET && a.reset[batch * a.time + t0 - min(s, last)];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           float sg, sc;
@@ -430,28 +448,34 @@ __global__ __launch_bounds__(256) void scan_backward_kernel(ScanLaunch l, Tiling
       }
       compose<V, CH>(sh, p);
       if constexpr (PAIRS) {
-        leave_pair<CH>(sh, tl, batch, j, at.first, a.chan);
+        leave_pair<V, PART>(sh, tl, batch, j, pl.first, a.chan);
       } else {
         float c[V], dfl[V];
         states_of_groups<V, CH>(sh, before, c);
+        // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
+        char *pdg = at<F32>(d.dg, batch * d.dg_batch + t0 * d.dg_time + pl.col);
+        char *pdu = at<F32>(d.du, batch * d.du_batch + t0 * d.du_time + pl.col);
 #pragma unroll
         for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          const int64_t t = last - s;
-          if (t < 0) break;
+          if (s >= more) break;
           float prior[V], dg[V], du[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) prior[i] = y[s].get(i);
-          if (t == 0) load_f32<V>(a.h0, batch * a.chan + at.col, at.cnt, prior);
+          if (t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior);
           backward_step<F32>(g[s], u[s], dy[s], prior, RESET && cut[s], fl, c, dg, du, dfl);
-          store<F32>(d.dg, batch * d.dg_batch + t * d.dg_time + at.col, at.cnt, dg);
-          store<F32>(d.du, batch * d.du_batch + t * d.du_time + at.col, at.cnt, du);
-          if (t == 0 && d.dh0)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-              if (i < at.cnt) d.dh0[batch * a.chan + at.col + i] = c[i];
+          store<F32>(at<F32>(pdg, -s * d.dg_time), pl.own, pl.cnt, dg);
+          store<F32>(at<F32>(pdu, -s * d.du_time), pl.own, pl.cnt, du);
         }
+        if (d.dh0 && steps > 0 && steps <= kSteps)   // the thread with the first step
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i >= pl.own && i < pl.cnt) d.dh0[batch * a.chan + pl.col + i] = c[i];
         if (d.dfloor) {   // the tile's sum over its steps, per channel
           __syncthreads();
 #pragma unroll
@@ -463,11 +487,13 @@ __global__ __launch_bounds__(256) void scan_backward_kernel(ScanLaunch l, Tiling
           for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
           sh.first[seg][ch] = sum;
           __syncthreads();
-          if (threadIdx.x < CH && at.first + ch < a.chan) {
+          if (threadIdx.x < CH) {
+            bool own;
+            const int64_t chan = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
             sum = 0.0f;
 #pragma unroll
             for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
-            floors[(batch * tl.chunks + j) * a.chan + at.first + ch] = sum;
+            if (own) floors[(batch * tl.chunks + j) * a.chan + chan] = sum;
           }
         }
       }
@@ -475,31 +501,36 @@ __global__ __launch_bounds__(256) void scan_backward_kernel(ScanLaunch l, Tiling
     }
 }
 
-template <bool F32>
+template <bool F32, bool PART>
 __global__ __launch_bounds__(64) void scan_backward_short_kernel(ScanLaunch l, int64_t threads, float *floors) {
   constexpr int V = Raw<F32>::V;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
-  const int64_t per = (a.chan + V - 1) / V;
+  const int64_t per = PART ? (a.chan + V - 1) / V : a.chan / V;
   for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
     const int64_t b = i / per, col = i % per * V;
     const int cnt = (int)min((int64_t)V, a.chan - col);
     float fl[V], c[V], dfl[V];
-    load_f32<V>(a.floor, col, cnt, fl);
-    load_f32<V>(d.dh_last, b * a.chan + col, cnt, c);
+    load_f32<V, PART>(a.floor, col, cnt, fl);
+    load_f32<V, PART>(d.dh_last, b * a.chan + col, cnt, c);
 #pragma unroll
     for (int k = 0; k < V; ++k) dfl[k] = 0.0f;
     for (int64_t t = a.time - 1; t >= 0; --t) {
-      Raw<F32> g, u, dy;
-      g.zero(); u.zero(); dy.zero();
-      g.load(a.g, b * a.g_batch + t * a.g_time + col, cnt);
-      u.load(a.u, b * a.u_batch + t * a.u_time + col, cnt);
-      dy.load(d.dy, b * d.dy_batch + t * d.dy_time + col, cnt);
+      Raw<F32> g, u, dy, y;
+      g.template load<PART>(at<F32>(a.g, b * a.g_batch + t * a.g_time + col), cnt);
+      u.template load<PART>(at<F32>(a.u, b * a.u_batch + t * a.u_time + col), cnt);
+      dy.template load<PART>(at<F32>(d.dy, b * d.dy_batch + t * d.dy_time + col), cnt);
       float before[V], dg[V], du[V];
-      state_before_step<F32>(a, b, t, col, cnt, before);
+      if (t > 0) {
+        y.template load<PART>(at<F32>(a.y, b * a.y_batch + (t - 1) * a.y_time + col), cnt);
+#pragma unroll
+        for (int k = 0; k < V; ++k) before[k] = y.get(k);
+      } else {
+        load_f32<V, PART>(a.h0, b * a.chan + col, cnt, before);
+      }
       backward_step<F32>(g, u, dy, before, a.reset && a.reset[b * a.time + t], fl, c, dg, du, dfl);
-      store<F32>(d.dg, b * d.dg_batch + t * d.dg_time + col, cnt, dg);
-      store<F32>(d.du, b * d.du_batch + t * d.du_time + col, cnt, du);
+      store<F32>(at<F32>(d.dg, b * d.dg_batch + t * d.dg_time + col), 0, cnt, dg);
+      store<F32>(at<F32>(d.du, b * d.du_batch + t * d.du_time + col), 0, cnt, du);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -566,61 +597,73 @@ hipError_t launch_states(const nvfp4_scan_args &a, const Tiling &t, const float 
   return hipGetLastError();
 }
 
-template <bool F32, bool RESET>
+template <bool F32, bool RESET, bool PART>
 hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
   const Tiling t = tiling_of(l, s.ws);
   const int ch = 8 * Raw<F32>::V;
   hipError_t e;
   if (l.chunks > 1) {
-    scan_forward_kernel<F32, RESET, true><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s.a, t);
+    scan_forward_kernel<F32, RESET, true, PART><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s.a, t);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_states(s.a, t, s.a.h0, stream)) != hipSuccess) return e;
   }
-  scan_forward_kernel<F32, RESET, false><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s.a, t);
+  scan_forward_kernel<F32, RESET, false, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s.a, t);
   return hipGetLastError();
 }
 
-template <bool F32, bool RESET>
+template <bool F32, bool RESET, bool PART>
 hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
   const Tiling t = tiling_of(l, s.ws);
   const int ch = 8 * Raw<F32>::V;
   hipError_t e;
   if (l.chunks > 1) {
-    scan_backward_kernel<F32, RESET, true><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s, t, floors);
+    scan_backward_kernel<F32, RESET, true, PART><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s, t, floors);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_states(s.a, t, s.d.dh_last, stream)) != hipSuccess) return e;
   }
-  scan_backward_kernel<F32, RESET, false><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s, t, floors);
+  scan_backward_kernel<F32, RESET, false, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s, t, floors);
   return hipGetLastError();
 }
 
 template <bool F32>
 hipError_t run_forward(const ScanLaunch &s, hipStream_t stream) {
+  constexpr int V = Raw<F32>::V;
   const nvfp4_scan_args &a = s.a;
-  if (a.time <= kShort) {
-    const int64_t threads = a.batch * ((a.chan + Raw<F32>::V - 1) / Raw<F32>::V);
-    scan_forward_short_kernel<F32><<<at_most((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(a, threads);
+  const bool few = a.chan < V;   // fewer channels than one access covers
+  if (a.time <= kShort) {   // (threads of whole accesses: where channels are left over, all in parts)
+    const int64_t threads = a.batch * ((a.chan + V - 1) / V);
+    const uint32_t grid = at_most((threads + 63) / 64, 64 * kCus);
+    if (a.chan % V) scan_forward_short_kernel<F32, true><<<grid, 64, 0, stream>>>(a, threads);
+    else scan_forward_short_kernel<F32, false><<<grid, 64, 0, stream>>>(a, threads);
     return hipGetLastError();
   }
   const Layout l = layout_of(a.batch, a.time, a.chan, false);
-  return a.reset ? forward_tiles<F32, true>(s, l, stream) : forward_tiles<F32, false>(s, l, stream);
+  if (a.reset) return few ? forward_tiles<F32, true, true>(s, l, stream) : forward_tiles<F32, true, false>(s, l, stream);
+  return few ? forward_tiles<F32, false, true>(s, l, stream) : forward_tiles<F32, false, false>(s, l, stream);
 }
 
 template <bool F32>
 hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
+  constexpr int V = Raw<F32>::V;
   const nvfp4_scan_args &a = s.a;
+  const bool few = a.chan < V;
   const Layout l = layout_of(a.batch, a.time, a.chan, true);
   float *floors = reinterpret_cast<float *>(static_cast<char *>(s.ws) + l.floors);
   hipError_t e = hipSuccess;
   if (a.batch > 0) {
     if (a.time <= kShort) {
-      const int64_t threads = a.batch * ((a.chan + Raw<F32>::V - 1) / Raw<F32>::V);
-      scan_backward_short_kernel<F32><<<at_most((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(
-          s, threads, a.time && s.d.dfloor ? floors : nullptr);   // (no steps: no workspace)
+      const int64_t threads = a.batch * ((a.chan + V - 1) / V);
+      const uint32_t grid = at_most((threads + 63) / 64, 64 * kCus);
+      float *sums = a.time && s.d.dfloor ? floors : nullptr;   // (no steps: no workspace)
+      if (a.chan % V) scan_backward_short_kernel<F32, true><<<grid, 64, 0, stream>>>(s, threads, sums);
+      else scan_backward_short_kernel<F32, false><<<grid, 64, 0, stream>>>(s, threads, sums);
       e = hipGetLastError();
+    } else if (a.reset) {
+      e = few ? backward_tiles<F32, true, true>(s, l, floors, stream)
+              : backward_tiles<F32, true, false>(s, l, floors, stream);
     } else {
-      e = a.reset ? backward_tiles<F32, true>(s, l, floors, stream)
-                  : backward_tiles<F32, false>(s, l, floors, stream);
+      e = few ? backward_tiles<F32, false, true>(s, l, floors, stream)
+              : backward_tiles<F32, false, false>(s, l, floors, stream);
     }
     if (e != hipSuccess) return e;
   }
