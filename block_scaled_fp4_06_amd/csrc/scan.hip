@@ -118,6 +118,17 @@ __device__ __forceinline__ void sigmoids(float g, float &s, float &sc) {
   sc = g < 0.0f ? 1.0f - s : e * s;
 }
 
+// The decay a = floor + (1 - floor) sigmoid(g) and 1 - a, in fewer instructions: the
+// exponential stops at 2^125, so sigmoid(g) ends at 2^-125 instead of zero, which adds
+// nothing to a sum with (1 - a) u.  (minimum, unlike min, lets a NaN through.)
+template <bool FLOOR>
+__device__ __forceinline__ void decay(float g, float fl, float &a, float &w) {
+  const float e = __builtin_elementwise_minimum(__expf(-g), 0x1p125f);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e), sc = e * s;
+  a = FLOOR ? __builtin_fmaf(1.0f - fl, s, fl) : s;
+  w = FLOOR ? (1.0f - fl) * sc : sc;
+}
+
 __device__ __forceinline__ float cut_mark() { return -0.0f; }
 __device__ __forceinline__ bool is_cut(float a) { return __float_as_uint(a) == 0x80000000u; }
 
@@ -223,19 +234,6 @@ __device__ __forceinline__ void states_of_groups(Shared<CH> &sh, float before, f
     h[i] = apply(sh.group[group][lane * V + i], sh.first[group / Shared<CH>::kPer][lane * V + i]);
 }
 
-// The tile's pair, from the first kernel to the second.
-template <int V, bool PART>
-__device__ __forceinline__ void leave_pair(Shared<8 * V> &sh, const Tiling &t, int64_t batch, int64_t j,
-                                           int64_t first, int64_t chan) {
-  if (threadIdx.x >= 8 * V) return;
-  bool own;
-  const int64_t c = channel_of<V, PART>(threadIdx.x, first, chan, own);
-  Pair all = sh.seg[0][threadIdx.x];
-#pragma unroll
-  for (int s = 1; s < Shared<8 * V>::kSegs; ++s) all = then(all, sh.seg[s][threadIdx.x]);
-  if (own) t.pairs[(batch * t.chunks + j) * chan + c] = all;
-}
-
 // The state before a tile: the second kernel's, or before the first tile the given one.
 template <int V, bool PART>
 __device__ __forceinline__ float state_before_tile(const Tiling &t, const float *given, int64_t batch,
@@ -248,19 +246,83 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, const float 
   return given ? given[batch * chan + c] : 0.0f;
 }
 
+// The first kernel: the pairs of all tiles but the last, which are whole.  A wave per tile,
+// kTile / 8 steps of V channels to a lane, four at a time with the next four's loads in
+// flight; the 8 groups of lanes are composed through LDS.  BACK: time runs backward, the
+// carries are c -> a (c + dy); `other` is dy, otherwise u.
+template <bool F32, bool BACK, bool RESET, bool FLOOR, bool PART>
+__global__ __launch_bounds__(64) void scan_pairs_kernel(nvfp4_scan_args a, const void *other,
+                                                        int64_t other_batch, int64_t other_time,
+                                                        Tiling tl) {
+  constexpr int V = Raw<F32>::V, CH = 8 * V, kLong = kTile / 8, kAhead = 4;
+  __shared__ Pair groups[8][CH];
+  const Place<V, PART> pl(a.chan);
+  const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
+  float fl[V];
+  if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
+  for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
+    for (int64_t j = blockIdx.y; j < tl.chunks - 1; j += gridDim.y) {
+      const int64_t i0 = j * kTile + group * kLong, t0 = BACK ? a.time - 1 - i0 : i0;
+      const int64_t sg = BACK ? -a.g_time : a.g_time, so = BACK ? -other_time : other_time;
+      const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
+      const char *po = at<F32>(other, batch * other_batch + t0 * other_time + pl.col);
+      Raw<F32> g[2][kAhead], o[2][kAhead];
+      auto fetch = [&](int q) {
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+          g[q & 1][s].template load<PART>(at<F32>(pg, (q * kAhead + s) * sg), pl.cnt);
+          o[q & 1][s].template load<PART>(at<F32>(po, (q * kAhead + s) * so), pl.cnt);
+        }
+      };
+      fetch(0);
+      Pair p[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < kLong / kAhead; ++q) {
+        if (q + 1 < kLong / kAhead) fetch(q + 1);
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+          const int64_t t = t0 + (BACK ? -1 : 1) * (q * kAhead + s);
+          const bool cut = RESET && (!PART || a.reset) && a.reset[batch * a.time + t];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float x, w;
+            decay<FLOOR>(g[q & 1][s].get(i), fl[i], x, w);
+            const float v = o[q & 1][s].get(i);
+            p[i] = Pair{x * p[i].a, BACK ? x * (p[i].b + v) : __builtin_fmaf(x, p[i].b, w * v)};
+            if (RESET && cut) p[i] = Pair{cut_mark(), BACK ? 0.0f : v};
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) groups[group][lane * V + i] = p[i];
+      __syncthreads();   // (one wave)
+      if (threadIdx.x < CH) {
+        bool own;
+        const int64_t c = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
+        Pair all = groups[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) all = then(all, groups[k][threadIdx.x]);
+        if (own) tl.pairs[(batch * tl.chunks + j) * a.chan + c] = all;
+      }
+      __syncthreads();
+    }
+}
+
 // The second kernel: a thread per batch row and channel walks over the tiles.
 __global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *given, int64_t chan,
                                                          int64_t threads) {
   for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
     const int64_t base = i / chan * t.chunks * chan + i % chan;
     float h = given ? given[i] : 0.0f;
-    for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += 16) {
-      Pair p[16];
+    for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += 32) {
+      Pair p[32];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
+      for (int k = 0; k < 32; ++k)
         if (j0 + k + 1 < t.chunks) p[k] = t.pairs[base + (j0 + k) * chan];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < 32; ++k) {
         if (j0 + k + 1 >= t.chunks) continue;
         h = apply(p[k], h);
         t.states[base + (j0 + k + 1) * chan] = h;
@@ -270,18 +332,18 @@ __global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *
 }
 
 // ---------------------------------------------------------------- forward
-// PAIRS: the first kernel (all tiles but the last); otherwise the third.  Steps past the end
-// (all in the last tile) read the last one again and lead nowhere.
-template <bool F32, bool RESET, bool PAIRS, bool PART>
+// The third kernel.  Steps past the end (all in the last tile) read the last one again and
+// lead nowhere.
+template <bool F32, bool RESET, bool FLOOR, bool PART>
 __global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   __shared__ Shared<CH> sh;
   const Place<V, PART> pl(a.chan);
   const int group = threadIdx.x >> 3;
   float fl[V];
-  load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
+  if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
   for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
-    for (int64_t j = blockIdx.y; j < tl.chunks - PAIRS; j += gridDim.y) {
+    for (int64_t j = blockIdx.y; j < tl.chunks; j += gridDim.y) {
       const int64_t t0 = min(j * kTile + group * kSteps, a.time - 1);
       const int more = (int)min((int64_t)kSteps, a.time - (j * kTile + group * kSteps));   // steps there are
       const int last = max(0, more - 1);
@@ -293,7 +355,7 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Ti
         g[s].template load<PART>(at<F32>(pg, min(s, last) * a.g_time), pl.cnt);
         u[s].template load<PART>(at<F32>(pu, min(s, last) * a.u_time), pl.cnt);
       }
-      const float before = PAIRS ? 0.0f : state_before_tile<V, PART>(tl, a.h0, batch, j, pl.first, a.chan);
+      const float before = state_before_tile<V, PART>(tl, a.h0, batch, j, pl.first, a.chan);
       float av[kSteps][V], bv[kSteps][V];
       Pair p[V];
 #pragma unroll
@@ -301,41 +363,36 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Ti
       bool cut[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        cut[s] = RESET && a.reset[batch * a.time + t0 + min(s, last)];
+        cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 + min(s, last)];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          float sg, sc;
-          sigmoids(g[s].get(i), sg, sc);
-          const float uv = u[s].get(i), rest = 1.0f - fl[i];
-          av[s][i] = __builtin_fmaf(rest, sg, fl[i]);
-          bv[s][i] = rest * sc * uv;
+          float w;
+          decay<FLOOR>(g[s].get(i), fl[i], av[s][i], w);
+          const float uv = u[s].get(i);
+          bv[s][i] = w * uv;
           if (RESET && cut[s]) bv[s][i] = uv;
           p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
           if (RESET && cut[s]) p[i] = Pair{cut_mark(), bv[s][i]};
         }
       }
       compose<V, CH>(sh, p);
-      if constexpr (PAIRS) {
-        leave_pair<V, PART>(sh, tl, batch, j, pl.first, a.chan);
-      } else {
-        float h[V];
-        states_of_groups<V, CH>(sh, before, h);
-        char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
+      float h[V];
+      states_of_groups<V, CH>(sh, before, h);
+      char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          if (s >= more) break;
+      for (int s = 0; s < kSteps; ++s) {
+        if (s >= more) break;
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
-            if (RESET && cut[s]) h[i] = bv[s][i];
-          }
-          store<F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
+        for (int i = 0; i < V; ++i) {
+          h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
+          if (RESET && cut[s]) h[i] = bv[s][i];
         }
-        if (a.h_last && j + 1 == tl.chunks && more > 0 && more <= kSteps && t0 + more == a.time)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
+        store<F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
       }
+      if (a.h_last && j + 1 == tl.chunks && more > 0 && more <= kSteps && t0 + more == a.time)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
       __syncthreads();   // before the next tile writes the shared words
     }
 }
@@ -374,7 +431,7 @@ __global__ __launch_bounds__(64) void scan_forward_short_kernel(nvfp4_scan_args 
 
 // ---------------------------------------------------------------- backward
 // One step: from dy and the carry c to dg, du and the next carry; adds to dfloor.
-template <bool F32>
+template <bool F32, bool FLOOR>
 __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> &u, const Raw<F32> &dy,
                                               const float (&before)[Raw<F32>::V], bool cut,
                                               const float (&fl)[Raw<F32>::V], float (&c)[Raw<F32>::V],
@@ -384,19 +441,18 @@ __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> 
   for (int i = 0; i < Raw<F32>::V; ++i) {
     float s, sc;
     sigmoids(g.get(i), s, sc);
-    const float rest = 1.0f - fl[i], grad = dy.get(i) + c[i], w = rest * sc;
+    const float rest = 1.0f - fl[i], grad = dy.get(i) + c[i], w = FLOOR ? rest * sc : sc;
     const float da = grad * (before[i] - u.get(i));
     du[i] = cut ? grad : w * grad;
     dg[i] = cut ? 0.0f : da * (w * s);
-    dfl[i] = __builtin_fmaf(cut ? 0.0f : da, sc, dfl[i]);
-    c[i] = cut ? 0.0f : __builtin_fmaf(rest, s, fl[i]) * grad;
+    if constexpr (FLOOR) dfl[i] = __builtin_fmaf(cut ? 0.0f : da, sc, dfl[i]);
+    c[i] = cut ? 0.0f : (FLOOR ? __builtin_fmaf(rest, s, fl[i]) : s) * grad;
   }
 }
 
 // Time runs backward: a thread's step s is t = time - 1 - (j kTile + group kSteps + s).
-// PAIRS: the first kernel, of the carries c -> a (c + dy), from g and dy; otherwise the third.
 // Steps before the beginning (all in the last tile) read the first one again and lead nowhere.
-template <bool F32, bool RESET, bool PAIRS, bool PART>
+template <bool F32, bool RESET, bool FLOOR, bool PART>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   __shared__ Shared<CH> sh;
@@ -405,9 +461,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void s
   const Place<V, PART> pl(a.chan);
   const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
   float fl[V];
-  load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
+#pragma unroll
+  for (int i = 0; i < V; ++i) fl[i] = 0.0f;
+  if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
   for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
-    for (int64_t j = blockIdx.y; j < tl.chunks - PAIRS; j += gridDim.y) {
+    for (int64_t j = blockIdx.y; j < tl.chunks; j += gridDim.y) {
       const int64_t steps = a.time - (j * kTile + group * kSteps);   // from the thread's first on
       const int64_t t0 = max((int64_t)0, steps - 1);
       const int more = (int)min((int64_t)kSteps, steps), last = max(0, more - 1);
@@ -419,82 +477,75 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void s
         g[s].template load<PART>(at<F32>(pg, -min(s, last) * a.g_time), pl.cnt);
         dy[s].template load<PART>(at<F32>(pdy, -min(s, last) * d.dy_time), pl.cnt);
       }
-      if constexpr (!PAIRS) {
-        const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
-        const char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
-        const int prior = (int)min((int64_t)kSteps, t0);   // (before the first step there is h0)
+      const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
+      const char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
+      const int prior = (int)min((int64_t)kSteps, t0);   // (before the first step there is h0)
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          u[s].template load<PART>(at<F32>(pu, -min(s, last) * a.u_time), pl.cnt);
-          y[s].template load<PART>(at<F32>(py, -min(s + 1, prior) * a.y_time), pl.cnt);
-        }
+      for (int s = 0; s < kSteps; ++s) {
+        u[s].template load<PART>(at<F32>(pu, -min(s, last) * a.u_time), pl.cnt);
+        y[s].template load<PART>(at<F32>(py, -min(s + 1, prior) * a.y_time), pl.cnt);
       }
-      const float before = PAIRS ? 0.0f : state_before_tile<V, PART>(tl, d.dh_last, batch, j, pl.first, a.chan);
+      const float before = state_before_tile<V, PART>(tl, d.dh_last, batch, j, pl.first, a.chan);
       Pair p[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
       bool cut[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        cut[s] = RESET && a.reset[batch * a.time + t0 - min(s, last)];
+        cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 - min(s, last)];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          float sg, sc;
-          sigmoids(g[s].get(i), sg, sc);
-          const float x = __builtin_fmaf(1.0f - fl[i], sg, fl[i]);
+          float x, w;
+          decay<FLOOR>(g[s].get(i), fl[i], x, w);
           p[i] = Pair{x * p[i].a, x * (p[i].b + dy[s].get(i))};
           if (RESET && cut[s]) p[i] = Pair{cut_mark(), 0.0f};
         }
       }
       compose<V, CH>(sh, p);
-      if constexpr (PAIRS) {
-        leave_pair<V, PART>(sh, tl, batch, j, pl.first, a.chan);
-      } else {
-        float c[V], dfl[V];
-        states_of_groups<V, CH>(sh, before, c);
-        // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
+      float c[V], dfl[V];
+      states_of_groups<V, CH>(sh, before, c);
+      // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+      for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
-        char *pdg = at<F32>(d.dg, batch * d.dg_batch + t0 * d.dg_time + pl.col);
-        char *pdu = at<F32>(d.du, batch * d.du_batch + t0 * d.du_time + pl.col);
+        for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
+      char *pdg = at<F32>(d.dg, batch * d.dg_batch + t0 * d.dg_time + pl.col);
+      char *pdu = at<F32>(d.du, batch * d.du_batch + t0 * d.du_time + pl.col);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
+      for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          if (s >= more) break;
-          float prior[V], dg[V], du[V];
+      for (int s = 0; s < kSteps; ++s) {
+        if (s >= more) break;
+        float prior[V], dg[V], du[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) prior[i] = y[s].get(i);
-          if (t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior);
-          backward_step<F32>(g[s], u[s], dy[s], prior, RESET && cut[s], fl, c, dg, du, dfl);
-          store<F32>(at<F32>(pdg, -s * d.dg_time), pl.own, pl.cnt, dg);
-          store<F32>(at<F32>(pdu, -s * d.du_time), pl.own, pl.cnt, du);
-        }
-        if (d.dh0 && steps > 0 && steps <= kSteps)   // the thread with the first step
+        for (int i = 0; i < V; ++i) prior[i] = y[s].get(i);
+        if (t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior);
+        backward_step<F32, FLOOR>(g[s], u[s], dy[s], prior, RESET && cut[s], fl, c, dg, du, dfl);
+        store<F32>(at<F32>(pdg, -s * d.dg_time), pl.own, pl.cnt, dg);
+        store<F32>(at<F32>(pdu, -s * d.du_time), pl.own, pl.cnt, du);
+      }
+      if (d.dh0 && steps > 0 && steps <= kSteps)   // the thread with the first step
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i >= pl.own && i < pl.cnt) d.dh0[batch * a.chan + pl.col + i] = c[i];
-        if (d.dfloor) {   // the tile's sum over its steps, per channel
-          __syncthreads();
+        for (int i = 0; i < V; ++i)
+          if (i >= pl.own && i < pl.cnt) d.dh0[batch * a.chan + pl.col + i] = c[i];
+      if (d.dfloor) {   // the tile's sum over its steps, per channel
+        __syncthreads();
 #pragma unroll
-          for (int i = 0; i < V; ++i) sh.group[group][lane * V + i].a = dfl[i];
-          __syncthreads();
-          const int ch = threadIdx.x % CH, seg = threadIdx.x / CH;
-          float sum = 0.0f;
+        for (int i = 0; i < V; ++i) sh.group[group][lane * V + i].a = dfl[i];
+        __syncthreads();
+        const int ch = threadIdx.x % CH, seg = threadIdx.x / CH;
+        float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
-          sh.first[seg][ch] = sum;
-          __syncthreads();
-          if (threadIdx.x < CH) {
-            bool own;
-            const int64_t chan = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
-            sum = 0.0f;
+        for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
+        sh.first[seg][ch] = sum;
+        __syncthreads();
+        if (threadIdx.x < CH) {
+          bool own;
+          const int64_t chan = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
+          sum = 0.0f;
 #pragma unroll
-            for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
-            if (own) floors[(batch * tl.chunks + j) * a.chan + chan] = sum;
-          }
+          for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
+          if (own) floors[(batch * tl.chunks + j) * a.chan + chan] = sum;
         }
       }
       __syncthreads();   // before the next tile writes the shared words
@@ -528,7 +579,7 @@ __global__ __launch_bounds__(64) void scan_backward_short_kernel(ScanLaunch l, i
       } else {
         load_f32<V, PART>(a.h0, b * a.chan + col, cnt, before);
       }
-      backward_step<F32>(g, u, dy, before, a.reset && a.reset[b * a.time + t], fl, c, dg, du, dfl);
+      backward_step<F32, true>(g, u, dy, before, a.reset && a.reset[b * a.time + t], fl, c, dg, du, dfl);
       store<F32>(at<F32>(d.dg, b * d.dg_batch + t * d.dg_time + col), 0, cnt, dg);
       store<F32>(at<F32>(d.du, b * d.du_batch + t * d.du_time + col), 0, cnt, du);
     }
@@ -597,31 +648,33 @@ hipError_t launch_states(const nvfp4_scan_args &a, const Tiling &t, const float 
   return hipGetLastError();
 }
 
-template <bool F32, bool RESET, bool PART>
+template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
   const Tiling t = tiling_of(l, s.ws);
   const int ch = 8 * Raw<F32>::V;
   hipError_t e;
   if (l.chunks > 1) {
-    scan_forward_kernel<F32, RESET, true, PART><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s.a, t);
+    scan_pairs_kernel<F32, false, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks - 1, ch), 64, 0, stream>>>(
+        s.a, s.a.u, s.a.u_batch, s.a.u_time, t);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_states(s.a, t, s.a.h0, stream)) != hipSuccess) return e;
   }
-  scan_forward_kernel<F32, RESET, false, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s.a, t);
+  scan_forward_kernel<F32, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s.a, t);
   return hipGetLastError();
 }
 
-template <bool F32, bool RESET, bool PART>
+template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
   const Tiling t = tiling_of(l, s.ws);
   const int ch = 8 * Raw<F32>::V;
   hipError_t e;
   if (l.chunks > 1) {
-    scan_backward_kernel<F32, RESET, true, PART><<<tile_grid(s.a, l.chunks - 1, ch), 256, 0, stream>>>(s, t, floors);
+    scan_pairs_kernel<F32, true, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks - 1, ch), 64, 0, stream>>>(
+        s.a, s.d.dy, s.d.dy_batch, s.d.dy_time, t);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_states(s.a, t, s.d.dh_last, stream)) != hipSuccess) return e;
   }
-  scan_backward_kernel<F32, RESET, false, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s, t, floors);
+  scan_backward_kernel<F32, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s, t, floors);
   return hipGetLastError();
 }
 
@@ -638,8 +691,12 @@ hipError_t run_forward(const ScanLaunch &s, hipStream_t stream) {
     return hipGetLastError();
   }
   const Layout l = layout_of(a.batch, a.time, a.chan, false);
-  if (a.reset) return few ? forward_tiles<F32, true, true>(s, l, stream) : forward_tiles<F32, true, false>(s, l, stream);
-  return few ? forward_tiles<F32, false, true>(s, l, stream) : forward_tiles<F32, false, false>(s, l, stream);
+  if (few) return forward_tiles<F32, true, true, true>(s, l, stream);
+  if (a.reset)
+    return a.floor ? forward_tiles<F32, true, true, false>(s, l, stream)
+                   : forward_tiles<F32, true, false, false>(s, l, stream);
+  return a.floor ? forward_tiles<F32, false, true, false>(s, l, stream)
+                 : forward_tiles<F32, false, false, false>(s, l, stream);
 }
 
 template <bool F32>
@@ -658,12 +715,14 @@ hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
       if (a.chan % V) scan_backward_short_kernel<F32, true><<<grid, 64, 0, stream>>>(s, threads, sums);
       else scan_backward_short_kernel<F32, false><<<grid, 64, 0, stream>>>(s, threads, sums);
       e = hipGetLastError();
+    } else if (few) {
+      e = backward_tiles<F32, true, true, true>(s, l, floors, stream);
     } else if (a.reset) {
-      e = few ? backward_tiles<F32, true, true>(s, l, floors, stream)
-              : backward_tiles<F32, true, false>(s, l, floors, stream);
+      e = a.floor ? backward_tiles<F32, true, true, false>(s, l, floors, stream)
+                  : backward_tiles<F32, true, false, false>(s, l, floors, stream);
     } else {
-      e = few ? backward_tiles<F32, false, true>(s, l, floors, stream)
-              : backward_tiles<F32, false, false>(s, l, floors, stream);
+      e = a.floor ? backward_tiles<F32, false, true, false>(s, l, floors, stream)
+                  : backward_tiles<F32, false, false, false>(s, l, floors, stream);
     }
     if (e != hipSuccess) return e;
   }
