@@ -66,29 +66,45 @@ struct Raw {              // 8 elements as loaded
       }
     }
   }
+  // All eight, without a branch.
+  __device__ __forceinline__ void load8(const void *p, int64_t i) {
+    const Four *q = reinterpret_cast<const Four *>(static_cast<const char *>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+    for (int j = 0; j < kWords / 4; ++j) {
+      const Four v = q[j];
+#pragma unroll
+      for (int l = 0; l < 4; ++l) w[4 * j + l] = v.w[l];
+    }
+  }
   __device__ __forceinline__ float get(int j) const {
     if constexpr (F32) return __uint_as_float(w[j]);
     else return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
   }
 };
 
+// Two bf16 values in a word, nearest-even.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef __bf16 Two __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, Two{(__bf16)lo, (__bf16)hi});
+}
+
+// Elements from `own` to cnt - 1 of the 8 at p[i].
 template <bool F32>
-__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const float (&v)[8]) {
-  if (cnt >= 8) {
+__device__ __forceinline__ void store(void *p, int64_t i, int cnt, const float (&v)[8], int own = 0) {
+  if (own <= 0 && cnt >= 8) {
     Four *q = reinterpret_cast<Four *>(static_cast<char *>(p) + i * (F32 ? 4 : 2));
 #pragma unroll
     for (int j = 0; j < (F32 ? 2 : 1); ++j) {
       Four f;
 #pragma unroll
       for (int l = 0; l < 4; ++l)
-        f.w[l] = F32 ? __float_as_uint(v[4 * j + l])
-                     : (uint32_t)bf16_bits_rn(v[2 * l]) | ((uint32_t)bf16_bits_rn(v[2 * l + 1]) << 16);
+        f.w[l] = F32 ? __float_as_uint(v[4 * j + l]) : pack2(v[2 * l], v[2 * l + 1]);
       q[j] = f;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (j >= cnt) continue;
+      if (j < own || j >= cnt) continue;
       if constexpr (F32) static_cast<float *>(p)[i + j] = v[j];
       else static_cast<uint16_t *>(p)[i + j] = bf16_bits_rn(v[j]);
     }
@@ -148,16 +164,16 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[16][N], int
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if (waves == 1) return;
-  const int wave = threadIdx.x >> 6;
+  const int first = threadIdx.y * waves;
   if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) part[turn][wave][i] = v[i];
+    for (int i = 0; i < N; ++i) part[turn][first + (threadIdx.x >> 6)][i] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = part[turn][0][i];
+  for (int i = 0; i < N; ++i) v[i] = part[turn][first][i];
   for (int w = 1; w < waves; ++w)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += part[turn][w][i];
+    for (int i = 0; i < N; ++i) v[i] += part[turn][first + w][i];
   turn ^= 1;
 }
 
@@ -291,30 +307,39 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
 // ---------------------------------------------------------------- backward
 constexpr int kMaxRow = 8192;     // columns of a row that one workgroup holds: 1024 x 8
 
-// How the rows are shared out among slots.  A slot has whole groups (rows that share a gate
-// row), or, where groups are fewer than the slots wanted, an even part of one group.
+// How the rows are shared out among slots, ranges of rows that one workgroup or one of its
+// `streams` walks over.  A slot has whole groups (rows that share a gate row), or, where
+// groups are fewer than the slots wanted, an even part of one group; the streams of a
+// workgroup then have parts of the same group.
 struct Split {
   int64_t rows, groups, slots;
-  int parts;        // slots per group; 1: a slot has whole groups
+  int parts;        // slots per group; 0: a slot has whole groups
+  int streams;      // slots per workgroup, whose sums leave it as one
+  int64_t sums;     // workgroups: rows of each result's sums in the workspace
 };
 
-__host__ __device__ inline Split split_rows(int64_t rows, int64_t groups, int64_t want) {
-  Split s = {rows, groups, 0, 1};
+__host__ __device__ inline Split split_rows(int64_t rows, int64_t groups, int streams, int64_t workgroups) {
+  Split s = {rows, groups, 0, 0, streams, 0};
+  int64_t want = workgroups * streams;
   if (want > rows) want = rows;
   if (groups >= want) {
     s.slots = want;
   } else {
     const int64_t per = rows / groups;
     int64_t parts = (want + groups - 1) / groups;
-    s.parts = (int)(parts < per ? parts : per);
+    if (parts > per) parts = per;
+    s.parts = (int)((parts + streams - 1) / streams * streams);   // (the last may be empty)
     s.slots = groups * s.parts;
   }
+  s.sums = (s.slots + streams - 1) / streams;
   return s;
 }
 
 __device__ __forceinline__ void slot_rows(const Split &s, int64_t slot, int64_t &r0, int64_t &r1) {
   const int64_t per = s.rows / s.groups;
-  if (s.parts == 1) {
+  if (slot >= s.slots) {
+    r0 = r1 = s.rows;
+  } else if (s.parts == 0) {
     r0 = slot * s.groups / s.slots * per;
     r1 = (slot + 1) * s.groups / s.slots * per;
   } else {
@@ -324,7 +349,24 @@ __device__ __forceinline__ void slot_rows(const Split &s, int64_t slot, int64_t 
   }
 }
 
-// What a thread keeps for its 8 columns: c + next; G = branch gate (c + post) of the current
+// Where a thread's 8 columns are.  Rows of 8 columns or more: the last threads of a row take
+// its last 8 elements, so that no load depends on a branch; their own are the elements
+// own .. 7 (none for a thread past the end), and the weights of the others are zero, which
+// keeps them out of every sum.  PART (fewer than 8 columns): cnt elements exist.
+template <bool PART>
+struct Place {
+  int col, own, cnt;
+  __device__ __forceinline__ Place(int at, int cols) : col(at), own(0), cnt(8) {
+    if constexpr (PART) {
+      cnt = cols - at;
+    } else if (at > cols - 8) {
+      own = min(8, at - (cols - 8));
+      col = cols - 8;
+    }
+  }
+};
+
+// What a thread keeps for its columns: c + next; G = branch gate (c + post) of the current
 // group; and the sums over rows.
 struct Columns {
   float wn[8], g[8];
@@ -337,29 +379,40 @@ struct Operands {         // one row's
   Raw<ZF> z, h;
 };
 
-// Slots' sums in the workspace: [dnext, dpost, dgate][slot][column].
-__device__ __forceinline__ float *slot_sums(void *ws, const Split &s, int which, int64_t slot, int cols) {
-  return static_cast<float *>(ws) + ((int64_t)which * s.slots + slot) * cols;
+// Workgroups' sums in the workspace: [dnext, dpost, dgate][workgroup][column].
+__device__ __forceinline__ float *sums_at(void *ws, const Split &s, int which, int64_t wg, int cols) {
+  return static_cast<float *>(ws) + ((int64_t)which * s.sums + wg) * cols;
 }
 
-template <bool XF, bool ZF>
-__device__ __forceinline__ void fetch_row(const nvfp4_norm_backward_args &a, int64_t row, int col,
-                                          int cnt, Operands<XF, ZF> &o) {
-  o.x.zero(); o.d.zero(); o.z.zero(); o.h.zero();
-  o.x.load(a.x_out, row * a.ld_x_out + col, cnt);
-  if (a.z) o.z.load(a.z, row * a.ld_z + col, cnt);
-  if (a.dx_out) o.d.load(a.dx_out, row * a.ld_dx_out + col, cnt);
-  if (a.next_weight) o.h.load(a.dh, row * a.ld_dh + col, cnt);
+template <bool PART, bool F32>
+__device__ __forceinline__ void fetch(const void *p, int64_t i, int cnt, Raw<F32> &r) {
+  if constexpr (PART) {
+    r.zero();
+    r.load(p, i, cnt);
+  } else {
+    r.load8(p, i);
+  }
+}
+
+template <bool PART, bool XF, bool ZF>
+__device__ __forceinline__ void fetch_row(const nvfp4_norm_backward_args &a, int64_t row,
+                                          const Place<PART> &at, Operands<XF, ZF> &o) {
+  o.d.zero(); o.z.zero(); o.h.zero();
+  fetch<PART>(a.x_out, row * a.ld_x_out + at.col, at.cnt, o.x);
+  if (a.z) fetch<PART>(a.z, row * a.ld_z + at.col, at.cnt, o.z);
+  if (a.dx_out) fetch<PART>(a.dx_out, row * a.ld_dx_out + at.col, at.cnt, o.d);
+  if (a.next_weight) fetch<PART>(a.dh, row * a.ld_dh + at.col, at.cnt, o.h);
 }
 
 // branch gate and c + post of a group (both zero without a branch).
-__device__ __forceinline__ void gate_and_post(const NormBackward &b, int64_t group, int col, int cnt,
+template <bool PART>
+__device__ __forceinline__ void gate_and_post(const NormBackward &b, int64_t group, const Place<PART> &at,
                                               float (&g)[8], float (&w)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) g[j] = w[j] = 0.0f;
   if (!b.a.z) return;
-  load_param(b.a.post_weight, b.p.weight_dtype, col, cnt, w);
-  if (b.a.gate) load_param(b.a.gate, b.p.gate_dtype, group * b.a.ld_gate + col, cnt, g);
+  load_param(b.a.post_weight, b.p.weight_dtype, at.col, at.cnt, w);
+  if (b.a.gate) load_param(b.a.gate, b.p.gate_dtype, group * b.a.ld_gate + at.col, at.cnt, g);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     w[j] += b.p.weight_offset;
@@ -367,48 +420,45 @@ __device__ __forceinline__ void gate_and_post(const NormBackward &b, int64_t gro
   }
 }
 
-__device__ __forceinline__ void open_group(const NormBackward &b, int64_t group, int col, int cnt,
+template <bool PART>
+__device__ __forceinline__ void open_group(const NormBackward &b, int64_t group, const Place<PART> &at,
                                            Columns &c) {
   float g[8], w[8];
-  gate_and_post(b, group, col, cnt, g, w);
+  gate_and_post(b, group, at, g, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    c.g[j] = g[j] * w[j];
+    c.g[j] = j < at.own ? 0.0f : g[j] * w[j];
     c.s[j] = 0.0f;
   }
 }
 
-__device__ __forceinline__ void open_slot(const NormBackward &b, int64_t group, int col, int cnt,
+template <bool PART>
+__device__ __forceinline__ void open_slot(const NormBackward &b, int64_t group, const Place<PART> &at,
                                           Columns &c) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) c.wn[j] = c.next[j] = c.post[j] = 0.0f;
   if (b.a.next_weight) {
-    load_param(b.a.next_weight, b.p.weight_dtype, col, cnt, c.wn);
+    load_param(b.a.next_weight, b.p.weight_dtype, at.col, at.cnt, c.wn);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c.wn[j] += b.p.weight_offset;
+    for (int j = 0; j < 8; ++j) c.wn[j] = j < at.own ? 0.0f : c.wn[j] + b.p.weight_offset;
   }
-  open_group(b, group, col, cnt, c);
+  open_group(b, group, at, c);
 }
 
-// The end of a group, or of a slot inside one: s goes into dpost and the gate's gradient.
-__device__ __forceinline__ void close_group(const NormBackward &b, const Split &s, int64_t slot,
-                                            int64_t group, int col, int cnt, Columns &c) {
+// The end of a group: s goes into dpost and, where the group was the slot's alone, the
+// gate's gradient (a part of a group leaves its s for close_slot).
+template <bool PART>
+__device__ __forceinline__ void close_group(const NormBackward &b, const Split &s, int64_t group,
+                                            const Place<PART> &at, Columns &c) {
   float g[8], w[8];
-  gate_and_post(b, group, col, cnt, g, w);
+  gate_and_post(b, group, at, g, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     c.post[j] += g[j] * c.s[j];
-    const float dg = b.p.branch_scale * w[j] * c.s[j];
-    if (!b.a.dgate || j >= cnt) continue;
-    if (s.parts == 1) store_param(b.a.dgate, b.p.gate_dtype, group * b.a.ld_dgate + col + j, dg);
-    else slot_sums(b.ws, s, 2, slot, (int)b.p.cols)[col + j] = dg;
+    c.s[j] *= b.p.branch_scale * w[j];
+    if (s.parts == 0 && b.a.dgate && j >= at.own && j < at.cnt)
+      store_param(b.a.dgate, b.p.gate_dtype, group * b.a.ld_dgate + at.col + j, c.s[j]);
   }
-}
-
-__device__ __forceinline__ void close_slot(const NormBackward &b, const Split &s, int64_t slot, int col,
-                                           int cnt, const Columns &c) {
-  if (b.a.dnext_weight) store<true>(slot_sums(b.ws, s, 0, slot, (int)b.p.cols), col, cnt, c.next);
-  if (b.a.dpost_weight) store<true>(slot_sums(b.ws, s, 1, slot, (int)b.p.cols), col, cnt, c.post);
 }
 
 // A thread's share of the three row sums.
@@ -427,9 +477,9 @@ __device__ __forceinline__ void partial_sums(const Operands<XF, ZF> &o, const Co
 
 // dx and dz of one row, and its terms of the sums over rows.  m1 = mean(t n) and
 // m2 = mean(G D n2).
-template <bool XF, bool ZF>
+template <bool PART, bool XF, bool ZF>
 __device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, const Operands<XF, ZF> &o,
-                                           int col, int cnt, float r, float rp, float m1, float m2,
+                                           const Place<PART> &at, float r, float rp, float m1, float m2,
                                            Columns &c) {
   const float skip = b.a.z ? b.p.skip_scale : 1.0f;
   float dx[8], dz[8];
@@ -442,57 +492,96 @@ __device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, c
     dx[j] = skip * d;
     dz[j] = rp * (c.g[j] * d - n2 * m2);
   }
-  store<XF>(b.a.dx, row * b.a.ld_dx + col, cnt, dx);
-  if (b.a.z) store<ZF>(b.a.dz, row * b.a.ld_dz + col, cnt, dz);
+  if (at.own >= 8) return;
+  store<XF>(b.a.dx, row * b.a.ld_dx + at.col, at.cnt, dx, at.own);
+  if (b.a.z) store<ZF>(b.a.dz, row * b.a.ld_dz + at.col, at.cnt, dz, at.own);
 }
 
-// Walks the rows of a slot: row(row, operands, columns) for each, the next row's operands in
-// flight, and the groups' ends between them.
-template <bool XF, bool ZF, class Row>
-__device__ __forceinline__ void walk_slot(const NormBackward &b, const Split &sp, int64_t slot, int col,
-                                          int cnt, Row &&do_row) {
-  const int64_t per = sp.rows / sp.groups;
-  int64_t row, end;
-  slot_rows(sp, slot, row, end);
-  int64_t group = row / per, left = (group + 1) * per - row;   // rows of the group from here on
-  Columns c;
-  open_slot(b, group, col, cnt, c);
-  Operands<XF, ZF> o, ahead;
-  fetch_row(b.a, row, col, cnt, ahead);
-  for (; row < end; ++row) {
-    o = ahead;
-    if (row + 1 < end) fetch_row(b.a, row + 1, col, cnt, ahead);
-    do_row(row, o, c);
-    if (--left == 0 || row + 1 == end) {
-      close_group(b, sp, slot, group, col, cnt, c);
+// Walks over `count` rows from `row` on (do_row for each that is before `end`: the streams
+// of a workgroup take the same number of turns), AHEAD rows' operands in flight, and the
+// groups' ends between them.
+template <int AHEAD, bool PART, bool XF, bool ZF, class Row>
+__device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp, int64_t row, int64_t end,
+                                          int64_t count, const Place<PART> &at, Columns &c, Row &&do_row) {
+  const int64_t per = sp.rows / sp.groups, last = max((int64_t)0, min(end, sp.rows) - 1);
+  int64_t group = min(row, last) / per, left = (group + 1) * per - row;   // rows of the group from here on
+  open_slot(b, group, at, c);
+  Operands<XF, ZF> o, ahead[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) fetch_row<PART>(b.a, min(row + k, last), at, ahead[k]);
+  for (int64_t i = 0; i < count; ++i, ++row) {
+    o = ahead[0];
+#pragma unroll
+    for (int k = 0; k + 1 < AHEAD; ++k) ahead[k] = ahead[k + 1];
+    if (i + AHEAD < count) fetch_row<PART>(b.a, min(row + AHEAD, last), at, ahead[AHEAD - 1]);
+    do_row(min(row, last), row < end, o);
+    if (row < end && (--left == 0 || row + 1 == end)) {
+      close_group(b, sp, group, at, c);
       if (row + 1 < end) {
-        open_group(b, ++group, col, cnt, c);
+        open_group(b, ++group, at, c);
         left = per;
       }
     }
   }
-  close_slot(b, sp, slot, col, cnt, c);
 }
 
-// A row per workgroup (or per wave, blockDim.y of them) at a time, a slot per workgroup (or
-// wave).  THREADS bounds the workgroup: fewer threads leave more registers to each.
-template <bool XF, bool ZF, int THREADS>
+// The sums of a workgroup's streams, added in order through LDS, into the workspace.  (A
+// stream's s is its share of dgate here, where groups are split.)
+template <bool PART>
+__device__ __forceinline__ void close_slots(const NormBackward &b, const Split &sp, int64_t wg,
+                                            const Place<PART> &at, Columns &c, float *lds) {
+  const int cols = (int)b.p.cols, y = threadIdx.y, streams = blockDim.y, tid = threadIdx.x, width = blockDim.x;
+#pragma unroll
+  for (int what = 0; what < 3; ++what) {
+    if (what == 0 ? !b.a.dnext_weight : what == 1 ? !b.a.dpost_weight : !(b.a.dgate && sp.parts)) continue;
+    float (&v)[8] = what == 0 ? c.next : what == 1 ? c.post : c.s;
+    if (streams > 1) {
+      __syncthreads();
+      if (y)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lds[((y - 1) * 8 + j) * width + tid] = v[j];
+      __syncthreads();
+      if (y) continue;
+      for (int k = 1; k < streams; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += lds[((k - 1) * 8 + j) * width + tid];
+    }
+    if (at.own < 8) store<true>(sums_at(b.ws, sp, what, wg, cols), at.col, at.cnt, v, at.own);
+  }
+}
+
+// blockDim = (64 waves, streams): a row per stream at a time.  THREADS bounds the workgroup:
+// fewer threads leave more registers to each.
+template <bool XF, bool ZF, int THREADS, bool PART>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, Split sp) {
   __shared__ float part[2][16][3];
-  const int cols = (int)b.p.cols, waves = blockDim.x >> 6;
-  const int64_t slot = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (slot >= sp.slots) return;   // (a whole wave where blockDim.y > 1; never otherwise)
+  extern __shared__ float lds[];
+  const int cols = (int)b.p.cols, waves = blockDim.x >> 6, streams = blockDim.y;
+  const int64_t slot = (int64_t)blockIdx.x * streams + threadIdx.y;
   const float scale = 1.0f / (float)cols;
-  const int col = (int)threadIdx.x * 8, cnt = cols - col;
+  const Place<PART> at((int)threadIdx.x * 8, cols);
   int turn = 0;
-  walk_slot<XF, ZF>(b, sp, slot, col, cnt, [&](int64_t row, const Operands<XF, ZF> &o, Columns &c) {
-    const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
+  int64_t row, end, count = 0;
+  slot_rows(sp, slot, row, end);
+  count = end - row;
+  if (waves > 1)   // every stream takes as many turns as the longest: they share barriers
+    for (int k = 0; k < streams; ++k) {
+      int64_t r0, r1;
+      slot_rows(sp, (int64_t)blockIdx.x * streams + k, r0, r1);
+      count = max(count, r1 - r0);
+    }
+  Columns c;
+  // (binary32 rows, and workgroups of over 640 threads, leave registers for one row ahead)
+  constexpr int kAhead = !XF && !ZF && THREADS <= 640 ? 2 : 1;
+  walk_rows<kAhead, PART, XF, ZF>(b, sp, row, end, count, at, c, [&](int64_t i, bool live, const Operands<XF, ZF> &o) {
+    const float r = b.a.next_weight ? b.a.rstd[i] : 0.0f, rp = b.a.z ? b.a.rstd_post[i] : 0.0f;
     float s[3] = {0.0f, 0.0f, 0.0f};
     partial_sums(o, c, r, rp, s);
     row_sum<3>(s, part, turn, waves);
     const float m1 = s[0] * scale, m2 = (s[1] - r * m1 * s[2]) * scale;
-    finish_row(b, row, o, col, cnt, r, rp, m1, m2, c);
+    if (live) finish_row(b, i, o, at, r, rp, m1, m2, c);
   });
+  close_slots(b, sp, blockIdx.x, at, c, lds);
 }
 
 // Long rows, first pass: m1 and m2 of every row, a workgroup per row at a time.
@@ -507,10 +596,11 @@ __global__ __launch_bounds__(512) void norm_means_kernel(NormBackward b, float *
     const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
     float s[3] = {0.0f, 0.0f, 0.0f};
     for (int col = (int)threadIdx.x * 8; col < cols; col += (int)blockDim.x * 8) {
+      const Place<false> at(col, cols);
       Operands<XF, ZF> o;
-      fetch_row(b.a, row, col, cols - col, o);
+      fetch_row(b.a, row, at, o);
       Columns c;
-      open_slot(b, row / per, col, cols - col, c);
+      open_slot(b, row / per, at, c);
       partial_sums(o, c, r, rp, s);
     }
     row_sum<3>(s, part, turn, waves);
@@ -527,17 +617,20 @@ template <bool XF, bool ZF>
 __global__ __launch_bounds__(256) void norm_strips_kernel(NormBackward b, Split sp, const float *means,
                                                           int strips) {
   const int64_t slot = blockIdx.x / strips;
-  const int col = (int)((blockIdx.x % strips) * 256 + threadIdx.x) * 8, cnt = (int)b.p.cols - col;
-  if (cnt <= 0) return;
-  walk_slot<XF, ZF>(b, sp, slot, col, cnt, [&](int64_t row, const Operands<XF, ZF> &o, Columns &c) {
-    const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
-    finish_row(b, row, o, col, cnt, r, rp, means[2 * row], means[2 * row + 1], c);
+  const Place<false> at((int)((blockIdx.x % strips) * 256 + threadIdx.x) * 8, (int)b.p.cols);
+  int64_t row, end;
+  slot_rows(sp, slot, row, end);
+  Columns c;
+  walk_rows<2, false, XF, ZF>(b, sp, row, end, end - row, at, c, [&](int64_t i, bool, const Operands<XF, ZF> &o) {
+    const float r = b.a.next_weight ? b.a.rstd[i] : 0.0f, rp = b.a.z ? b.a.rstd_post[i] : 0.0f;
+    finish_row(b, i, o, at, r, rp, means[2 * i], means[2 * i + 1], c);
   });
+  close_slots(b, sp, slot, at, c, nullptr);   // (one stream)
 }
 
-// The slots' sums added in order.  A workgroup has 32 columns of one result, 32 threads to a
-// column, each with a consecutive share of the slots: results 0 and 1 are dnext and dpost,
-// 2 + g the gate row g.
+// The workgroups' sums added in order.  A workgroup has 32 columns of one result, 32 threads
+// to a column, each with a consecutive share of the sums: results 0 and 1 are dnext and
+// dpost, 2 + g the gate row g.
 __global__ __launch_bounds__(1024) void norm_columns_kernel(NormBackward b, Split sp, int strips) {
   __shared__ float part[32][32];
   const int cols = (int)b.p.cols, lane = threadIdx.x & 31, share = threadIdx.x >> 5;
@@ -545,8 +638,9 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormBackward b, Spli
   const int64_t what = blockIdx.x / strips;
   void *out = what == 0 ? b.a.dnext_weight : what == 1 ? b.a.dpost_weight : b.a.dgate;
   if (!out) return;   // (the whole workgroup)
-  const int64_t first = what < 2 ? 0 : (what - 2) * sp.parts, count = what < 2 ? sp.slots : sp.parts;
-  const float *sums = slot_sums(b.ws, sp, what < 2 ? (int)what : 2, first, cols);
+  const int64_t per_group = sp.parts / sp.streams;
+  const int64_t first = what < 2 ? 0 : (what - 2) * per_group, count = what < 2 ? sp.sums : per_group;
+  const float *sums = sums_at(b.ws, sp, what < 2 ? (int)what : 2, first, cols);
   float v = 0.0f;
   if (c < cols) {
     const int64_t end = count * (share + 1) / 32;
@@ -582,13 +676,13 @@ int waves_of(int64_t cols, int each) { return (int)((cols + 64 * each - 1) / (64
 // Workgroups at a time on a CU of `threads` threads whose kernels use up to 128 registers.
 int resident(int threads) { return threads >= 1024 ? 1 : 1024 / threads; }
 
-int64_t slots_wanted(const nvfp4_norm_params &p) {
-  if (p.cols > kMaxRow) return 128;
-  const int waves = waves_of(p.cols, 8);
-  return (int64_t)kCus * (waves == 1 ? 4 : resident(64 * waves));
+// Short rows go several to a workgroup of up to 8 waves, so that their sums over rows are
+// added there.
+Split split_of(const nvfp4_norm_params &p) {
+  if (p.cols > kMaxRow) return split_rows(p.rows, p.gate_rows, 1, 128);
+  const int waves = waves_of(p.cols, 8), streams = waves <= 8 ? 8 / waves : 1;
+  return split_rows(p.rows, p.gate_rows, streams, kCus);
 }
-
-Split split_of(const nvfp4_norm_params &p) { return split_rows(p.rows, p.gate_rows, slots_wanted(p)); }
 
 template <bool XF, bool ZF, int K, bool HOLD>
 hipError_t run_forward(const NormForward &n, hipStream_t stream) {
@@ -610,15 +704,16 @@ hipError_t forward_of(const NormForward &n, hipStream_t stream) {
 template <bool XF, bool ZF>
 hipError_t backward_of(const NormBackward &b, const Split &sp, hipStream_t stream) {
   if (b.p.cols <= kMaxRow) {
-    const int waves = waves_of(b.p.cols, 8), y = waves == 1 ? 4 : 1;
-    const uint32_t grid = (uint32_t)((sp.slots + y - 1) / y);
-    if (waves <= 10)
-      norm_backward_kernel<XF, ZF, 640><<<grid, dim3(64 * waves, y), 0, stream>>>(b, sp);
-    else
-      norm_backward_kernel<XF, ZF, 1024><<<grid, dim3(64 * waves, y), 0, stream>>>(b, sp);
+    const int waves = waves_of(b.p.cols, 8);
+    const dim3 block(64 * waves, sp.streams);
+    const size_t lds = (size_t)(sp.streams - 1) * 8 * block.x * sizeof(float);
+    const uint32_t grid = (uint32_t)sp.sums;
+    if (b.p.cols < 8) norm_backward_kernel<XF, ZF, 640, true><<<grid, block, lds, stream>>>(b, sp);
+    else if (waves <= 10) norm_backward_kernel<XF, ZF, 640, false><<<grid, block, lds, stream>>>(b, sp);
+    else norm_backward_kernel<XF, ZF, 1024, false><<<grid, block, lds, stream>>>(b, sp);
     return hipGetLastError();
   }
-  float *means = static_cast<float *>(b.ws) + 3 * sp.slots * b.p.cols;
+  float *means = static_cast<float *>(b.ws) + 3 * sp.sums * b.p.cols;
   const int64_t wgs = b.p.rows < 4 * kCus ? b.p.rows : 4 * kCus;
   norm_means_kernel<XF, ZF><<<(uint32_t)wgs, 512, 0, stream>>>(b, means);
   const hipError_t e = hipGetLastError();
@@ -632,7 +727,7 @@ hipError_t backward_of(const NormBackward &b, const Split &sp, hipStream_t strea
 
 size_t norm_workspace_bytes(const nvfp4_norm_params &p) {
   const Split s = split_of(p);
-  return 4 * (3 * (size_t)s.slots * (size_t)p.cols + (p.cols > kMaxRow ? 2 * (size_t)p.rows : 0));
+  return 4 * (3 * (size_t)s.sums * (size_t)p.cols + (p.cols > kMaxRow ? 2 * (size_t)p.rows : 0));
 }
 
 hipError_t launch_norm_forward(const NormForward &n, hipStream_t stream) {
@@ -652,7 +747,7 @@ hipError_t launch_norm_backward(const NormBackward &b, hipStream_t stream) {
                                                       : backward_of<true, true>(b, sp, stream);
   if (e != hipSuccess || !sums) return e;
   const int strips = (int)((b.p.cols + 31) / 32);
-  const int64_t results = 2 + (b.a.dgate && sp.parts > 1 ? sp.groups : 0);
+  const int64_t results = 2 + (b.a.dgate && sp.parts ? sp.groups : 0);
   norm_columns_kernel<<<(uint32_t)(results * strips), 1024, 0, stream>>>(b, sp, strips);
   return hipGetLastError();
 }

@@ -2,47 +2,46 @@
 the memory it takes there, and the checks of its tensors."""
 from __future__ import annotations
 
-import contextlib
-
 from . import nvfp4 as N
 
-DTYPES = {"torch.bfloat16": 0, "torch.float32": 1}   # nvfp4_dtype
+_CODES = {}
 
 
 def dtype_code(name, t):
     """nvfp4_dtype of a tensor; ValueError unless it is bf16 or float32."""
-    code = DTYPES.get(str(t.dtype))
+    if not _CODES:   # (importing the package needs no torch)
+        import torch
+        _CODES.update({torch.bfloat16: 0, torch.float32: 1})
+    code = _CODES.get(t.dtype)
     if code is None:
         raise ValueError("%s has dtype %s, expected torch.bfloat16 or torch.float32" %
                          (name, t.dtype))
     return code
 
 
-@contextlib.contextmanager
-def on_stream(stream, device, inputs):
-    """Run a call on `stream` (None: the current stream of `device`) with `device` current.
+def run_on(stream, device, inputs, call):
+    """call(handle) on `stream` (None: the current stream of `device`) with `device` current.
 
-    Memory that the call allocates inside belongs to that stream, and the inputs are kept
-    from reuse until the stream has passed, so a call on a stream other than the one its
-    tensors were made on needs no more from the caller than the order of the work itself.
-    Yields the raw stream handle."""
+    Memory that the call allocates belongs to that stream, and the inputs are kept from reuse
+    until the stream has passed, so a call on a stream other than the one its tensors were
+    made on needs no more from the caller than the order of the work itself."""
     import torch
     N._require_gpu(device)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device), on_stream(stream, device, inputs) as handle:
-            yield handle
-        return
-    current = torch.cuda.current_stream(device)
-    if stream is None or stream == current:
-        yield current.cuda_stream
-        return
+    index = device.index
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(device):
+            return run_on(stream, device, inputs, call)
+    # (the handle alone: a Stream object costs more than a small call's own work)
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or stream.cuda_stream == current and stream.device == device:
+        return call(current)
     if stream.device != device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
     with torch.cuda.stream(stream):
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
-        yield stream.cuda_stream
+        return call(stream.cuda_stream)
 
 
 def check(rc, name):
@@ -51,4 +50,14 @@ def check(rc, name):
 
 
 def ptr(t):
-    return t.data_ptr() if t is not None and t.numel() else None
+    """Address of a tensor's first element; 0 (a null pointer) for None and for no elements."""
+    return 0 if t is None else t.data_ptr()
+
+
+def new_like(t):
+    """A new contiguous tensor of t's shape and type (None for None)."""
+    import torch
+    if t is None:
+        return None
+    return torch.empty_like(t) if t.is_contiguous() else (
+        torch.empty(t.shape, dtype=t.dtype, device=t.device))

@@ -24,7 +24,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 from . import nvfp4 as N
-from .launch import check, dtype_code, on_stream, ptr
+from .launch import check, dtype_code, new_like, ptr, run_on
 
 MAX_COLS = 32768
 
@@ -53,29 +53,31 @@ class ResidualNormGrads:
     dgate: Optional["object"]
 
 
-def _matrix(name, t, shape, like, dtype=None):
-    """t is a (rows, cols) tensor of `shape` on like's device with rows laid out apart."""
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+def _matrix(name, t, shape, device, dtype=None):
+    """t is a (rows, cols) tensor of `shape` on `device` with rows laid out apart."""
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    dtype_code(name, t)
-    if dtype is not None and t.dtype != dtype:
+    if dtype is None:
+        dtype_code(name, t)
+    elif t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != like.device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
-    rows, cols = t.shape
-    if (cols > 1 and rows and t.stride(1) != 1) or (rows > 1 and cols and t.stride(0) < cols):
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    rows, cols = shape
+    if not t.is_contiguous() and ((cols > 1 and rows and t.stride(1) != 1) or
+                                  (rows > 1 and cols and t.stride(0) < cols)):
         raise ValueError("%s must be row-major with unit column stride" % name)
 
 
-def _vector(name, t, n, like, dtype=None):
+def _vector(name, t, n, device, dtype=None):
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError("%s has shape %s, expected (%d,)" % (name, tuple(t.shape), n))
     if dtype is None:
         dtype_code(name, t)
-    elif t.dtype != dtype:
+    elif t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != like.device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
@@ -83,24 +85,25 @@ def _vector(name, t, n, like, dtype=None):
 def _check_operands(x, z, post_weight, next_weight, gate):
     if x.dim() != 2:
         raise ValueError("x must be 2-D, not %d-D" % x.dim())
-    rows, cols = x.shape
+    shape, device = x.shape, x.device
+    rows, cols = shape
     if cols > MAX_COLS:
         raise ValueError("x has %d columns, at most %d are supported" % (cols, MAX_COLS))
-    _matrix("x", x, x.shape, x)
+    _matrix("x", x, shape, device)
     if z is None:
         if post_weight is not None or gate is not None:
             raise ValueError("post_weight and gate need a branch z")
         if next_weight is None:
             raise ValueError("next_weight is missing")
     else:
-        _matrix("z", z, x.shape, x)
-        if str(x.dtype) == "torch.bfloat16" and z.dtype != x.dtype:
+        _matrix("z", z, shape, device)
+        if z.dtype is not x.dtype and dtype_code("x", x) == 0:
             raise ValueError("z has dtype %s, expected %s" % (z.dtype, x.dtype))
         if post_weight is None:
             raise ValueError("post_weight is missing")
-        _vector("post_weight", post_weight, cols, x)
+        _vector("post_weight", post_weight, cols, device)
     if next_weight is not None:
-        _vector("next_weight", next_weight, cols, x,
+        _vector("next_weight", next_weight, cols, device,
                 None if post_weight is None else post_weight.dtype)
     if gate is not None:
         if gate.dim() != 2:
@@ -108,20 +111,18 @@ def _check_operands(x, z, post_weight, next_weight, gate):
         g = gate.shape[0]
         if g < 1 or rows % g or (rows and g > rows):
             raise ValueError("gate has %d rows, which must divide the %d rows of x" % (g, rows))
-        _matrix("gate", gate, (g, cols), x)
+        _matrix("gate", gate, (g, cols), device)
 
 
-def _params(x, h_dtype_of, weight, gate, eps, ctx_or_scales):
-    offset, skip, branch = ctx_or_scales
-    return N.NormParams(x.shape[0], x.shape[1], gate.shape[0] if gate is not None else 1,
-                        dtype_code("x", x), dtype_code("z", h_dtype_of),
-                        dtype_code("weight", weight),
-                        dtype_code("gate", gate) if gate is not None else 0, eps, offset, skip,
-                        branch)
+def _params(x, h_type_of, weight, gate, eps, offset, skip, branch):
+    rows, cols = x.shape
+    return N.NormParams(rows, cols, 1 if gate is None else gate.shape[0], dtype_code("x", x),
+                        dtype_code("z", h_type_of), dtype_code("weight", weight),
+                        0 if gate is None else dtype_code("gate", gate), eps, offset, skip, branch)
 
 
 def _ld(t):
-    return t.stride(0) if t is not None and t.dim() == 2 and t.shape[0] > 1 else 0
+    return t.stride(0) if t is not None else 0
 
 
 def residual_norm_forward(x, z, post_weight, next_weight=None, gate=None, skip_scale=1.0,
@@ -135,23 +136,28 @@ def residual_norm_forward(x, z, post_weight, next_weight=None, gate=None, skip_s
         raise ValueError("z is missing (norm_forward is the norm without a branch)")
     _check_operands(x, z, post_weight, next_weight, gate)
     if out is not None:
-        _matrix("out", out, x.shape, x, x.dtype)
-    rows = x.shape[0]
-    with on_stream(stream, x.device, (x, z, post_weight, next_weight, gate, out)) as handle:
-        x_out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-        h = rstd = None
+        _matrix("out", out, x.shape, x.device, x.dtype)
+    ctx = ResidualNormContext(out, z, post_weight, next_weight, gate, None, None, skip_scale,
+                              branch_scale, weight_offset)
+
+    def call(handle):
+        dev, f32 = x.device, torch.float32
+        x_out = ctx.x_out = new_like(x) if out is None else out
+        ctx.rstd_post = torch.empty(x.shape[0], dtype=f32, device=dev)
+        h = None
         if next_weight is not None:
-            h, rstd = torch.empty(z.shape, dtype=z.dtype, device=x.device), stats[1]
-        prm = _params(x, z, post_weight, gate, eps, (weight_offset, skip_scale, branch_scale))
+            h = new_like(z)
+            ctx.rstd = torch.empty(x.shape[0], dtype=f32, device=dev)
+        prm = _params(x, z, post_weight, gate, eps, weight_offset, skip_scale, branch_scale)
         args = N.NormForwardArgs(ptr(x), _ld(x), ptr(z), _ld(z), ptr(post_weight), ptr(gate),
                                  _ld(gate), ptr(next_weight), ptr(x_out), _ld(x_out), ptr(h),
-                                 _ld(h), ptr(rstd), ptr(stats[0]))
+                                 _ld(h), ptr(ctx.rstd), ptr(ctx.rstd_post))
         check(N.nvfp4_residual_norm_forward(prm, args, handle), "nvfp4_residual_norm_forward")
+        return h
+    h = run_on(stream, x.device, (x, z, post_weight, next_weight, gate, out), call)
     if out is not None:
         torch.autograd.graph.increment_version(out)
-    return x_out, h, ResidualNormContext(x_out, z, post_weight, next_weight, gate, rstd, stats[0],
-                                         skip_scale, branch_scale, weight_offset)
+    return ctx.x_out, h, ctx
 
 
 def norm_forward(x, weight, eps=1e-6, weight_offset=0.0, out_dtype=None, stream=None):
@@ -163,13 +169,15 @@ def norm_forward(x, weight, eps=1e-6, weight_offset=0.0, out_dtype=None, stream=
     if out_dtype not in (torch.bfloat16, torch.float32) or (
             x.dtype == torch.bfloat16 and out_dtype != x.dtype):
         raise ValueError("out_dtype %s does not go with x of %s" % (out_dtype, x.dtype))
-    with on_stream(stream, x.device, (x, weight)) as handle:
+    def call(handle):
         h = torch.empty(x.shape, dtype=out_dtype, device=x.device)
         rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-        prm = _params(x, h, weight, None, eps, (weight_offset, 1.0, 1.0))
+        prm = _params(x, h, weight, None, eps, weight_offset, 1.0, 1.0)
         args = N.NormForwardArgs(x=ptr(x), ld_x=_ld(x), next_weight=ptr(weight), h=ptr(h),
                                  ld_h=_ld(h), rstd=ptr(rstd))
         check(N.nvfp4_residual_norm_forward(prm, args, handle), "nvfp4_residual_norm_forward")
+        return h, rstd
+    h, rstd = run_on(stream, x.device, (x, weight), call)
     return h, ResidualNormContext(x, None, None, weight, None, rstd, None, 1.0, 1.0, weight_offset)
 
 
@@ -180,28 +188,25 @@ def residual_norm_backward(dx_out, dh, ctx: ResidualNormContext, stream=None) ->
     x, z, gate = ctx.x_out, ctx.z, ctx.gate
     _check_operands(x, z, ctx.post_weight, ctx.next_weight, gate)
     rows, cols = x.shape
-    like = z if z is not None else dh
+    dev, f32 = x.device, torch.float32
     if dx_out is not None:
-        _matrix("dx_out", dx_out, x.shape, x, x.dtype)
+        _matrix("dx_out", dx_out, x.shape, dev, x.dtype)
     if (dh is None) != (ctx.next_weight is None):
         raise ValueError("dh must be given exactly when the forward call had next_weight")
     if dh is not None:
-        _matrix("dh", dh, x.shape, x, None if z is None else z.dtype)
-        _vector("rstd", ctx.rstd, rows, x, torch.float32)
+        _matrix("dh", dh, x.shape, dev, None if z is None else z.dtype)
+        _vector("rstd", ctx.rstd, rows, dev, f32)
     if z is not None:
-        _vector("rstd_post", ctx.rstd_post, rows, x, torch.float32)
-    weight = ctx.next_weight if ctx.post_weight is None else ctx.post_weight
-    inputs = (x, z, ctx.post_weight, ctx.next_weight, gate, ctx.rstd, ctx.rstd_post, dx_out, dh)
-    with on_stream(stream, x.device, inputs) as handle:
-        def new(shape, t):
-            return None if t is None else torch.empty(shape, dtype=t.dtype, device=x.device)
-        d = ResidualNormGrads(new(x.shape, x), new(x.shape, z), new((cols,), ctx.post_weight),
-                              new((cols,), ctx.next_weight),
-                              None if gate is None else new(gate.shape, gate))
-        prm = _params(x, like, weight, gate, 0.0,
-                      (ctx.weight_offset, ctx.skip_scale, ctx.branch_scale))
+        _vector("rstd_post", ctx.rstd_post, rows, dev, f32)
+
+    def call(handle):
+        d = ResidualNormGrads(new_like(x), new_like(z), new_like(ctx.post_weight),
+                              new_like(ctx.next_weight), new_like(gate))
+        prm = _params(x, dh if z is None else z,
+                      ctx.next_weight if ctx.post_weight is None else ctx.post_weight, gate, 0.0,
+                      ctx.weight_offset, ctx.skip_scale, ctx.branch_scale)
         need = N.nvfp4_residual_norm_workspace_bytes(prm)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
         args = N.NormBackwardArgs(ptr(x), _ld(x), ptr(z), _ld(z), ptr(ctx.post_weight), ptr(gate),
                                   _ld(gate), ptr(ctx.next_weight), ptr(ctx.rstd),
                                   ptr(ctx.rstd_post), ptr(dx_out), _ld(dx_out), ptr(dh), _ld(dh),
@@ -209,7 +214,9 @@ def residual_norm_backward(dx_out, dh, ctx: ResidualNormContext, stream=None) ->
                                   ptr(d.dnext_weight), ptr(d.dgate), _ld(d.dgate))
         check(N.nvfp4_residual_norm_backward(prm, args, ptr(ws), need, handle),
               "nvfp4_residual_norm_backward")
-    return d
+        return d
+    return run_on(stream, dev, (x, z, ctx.post_weight, ctx.next_weight, gate, ctx.rstd,
+                                ctx.rstd_post, dx_out, dh), call)
 
 
 def norm_backward(dh, ctx: ResidualNormContext, dresidual=None, stream=None):

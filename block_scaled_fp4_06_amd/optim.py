@@ -25,7 +25,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 from . import nvfp4 as N
-from .launch import check, dtype_code, on_stream, ptr
+from .launch import check, dtype_code, ptr, run_on
 
 BLOCK = 256   # elements of one block of 8-bit moments (NVFP4_ADAMW_BLOCK)
 
@@ -111,7 +111,7 @@ class AdamW:
         self.stochastic_rounding, self.seed = bool(stochastic_rounding), int(seed)
         self.state = state if state is not None else new_state(self.params, bits, master)
         self._check_state()
-        self._shapes = [(p.shape, p.numel()) for p in self.params]
+        self._shapes = [p.shape for p in self.params]
         self._table = None
 
     def _check_state(self):
@@ -137,7 +137,7 @@ class AdamW:
         pins = [p.data_ptr() for p in self.params]
         pins += [t.data_ptr() for t in (s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
                                         s.exp_avg_sq_scale, s.master) if t is not None]
-        kinds = [self.params[i].dtype if g is None else g.dtype for i, g in enumerate(grads)]
+        kinds = [p.dtype if g is None else g.dtype for g, p in zip(grads, self.params)]
         if self._table is not None and self._table[0] == pins and self._table[1] == kinds:
             return self._table
         self._check_state()
@@ -163,6 +163,22 @@ class AdamW:
         self._table = (pins, kinds, host, host.to(self.device))
         return self._table
 
+    def _check_grads(self, grads):
+        """One gradient (or None) per parameter: contiguous, of its shape, on its device."""
+        import torch
+        dev, kinds = self.device, (torch.bfloat16, torch.float32)
+        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+            if g is None:
+                continue
+            if g.shape != shape or not g.is_contiguous():
+                raise ValueError("grads[%d] must be a contiguous tensor of shape %s" %
+                                 (i, tuple(shape)))
+            if g.dtype not in kinds:
+                raise ValueError("grads[%d] has dtype %s, expected torch.bfloat16 or "
+                                 "torch.float32" % (i, g.dtype))
+            if g.device != dev:
+                raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
+
     def step(self, grads=None, lr=None, grad_scale=None, stream=None):
         """One update.  grads: a list like params (default: each parameter's .grad), contiguous,
         bf16 or float32; None leaves a parameter as it is.  grad_scale: a float32 tensor of one
@@ -173,28 +189,18 @@ class AdamW:
             grads = [p.grad for p in self.params]
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
-        bf16, f32, dev, pointers = torch.bfloat16, torch.float32, self.device, []
-        for i, (g, (shape, n)) in enumerate(zip(grads, self._shapes)):
-            if g is None:
-                pointers.append(None)
-                continue
-            if g.shape != shape or not g.is_contiguous():
-                raise ValueError("grads[%d] must be a contiguous tensor of shape %s" %
-                                 (i, tuple(shape)))
-            if g.dtype is not bf16 and g.dtype is not f32:
-                raise ValueError("grads[%d] has dtype %s, expected torch.bfloat16 or "
-                                 "torch.float32" % (i, g.dtype))
-            if g.device != dev:
-                raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
-            pointers.append(g.data_ptr() if n else None)
+        dev, f32 = self.device, torch.float32
+        self._check_grads(grads)
+        pointers = [0 if g is None else g.data_ptr() for g in grads]
         if grad_scale is not None:
             N._check_buffer("grad_scale", grad_scale.reshape(-1), (1,), (f32,), dev, False)
         if lr is not None:
             self.lr = lr
         s = self.state
-        used = (*grads, grad_scale, *self.params, s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
-                s.exp_avg_sq_scale, s.master)
-        with on_stream(stream, dev, used) as handle:
+        used = () if stream is None else (*grads, grad_scale, *self.params, s.exp_avg, s.exp_avg_sq,
+                                          s.exp_avg_scale, s.exp_avg_sq_scale, s.master)
+
+        def call(handle):
             _, _, host, device = self._layout(grads)
             prm = N.AdamWParams(self.lr, self.betas[0], self.betas[1], self.eps, s.step + 1,
                                 self.seed, 1 if self.stochastic_rounding else 0, 0,
@@ -202,7 +208,9 @@ class AdamW:
             check(N.nvfp4_adamw_step(host.data_ptr(), device.data_ptr(),
                                      (ctypes.c_void_p * len(pointers))(*pointers), prm, handle),
                   "nvfp4_adamw_step")
-            device.record_stream(torch.cuda.current_stream(dev))
+            if stream is not None:   # (the table may be remade before this stream has passed)
+                device.record_stream(stream)
+        run_on(stream, dev, used, call)
         torch.autograd.graph.increment_version(self.params)
         s.step += 1
 
@@ -217,11 +225,13 @@ class AdamW:
         if dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("dtype %s, expected torch.bfloat16 or torch.float32" % dtype)
         codes = (s.exp_avg, s.exp_avg_scale, s.exp_avg_sq, s.exp_avg_sq_scale)
-        with on_stream(stream, self.device, codes) as handle:
+
+        def call(handle):
             m = torch.empty(s.exp_avg.shape, dtype=dtype, device=self.device)
             v = torch.empty(s.exp_avg.shape, dtype=dtype, device=self.device)
             check(N.nvfp4_adamw_moments(ptr(codes[0]), ptr(codes[1]), ptr(codes[2]), ptr(codes[3]),
                                         m.numel(), ptr(m), ptr(v),
                                         1 if dtype == torch.float32 else 0, handle),
                   "nvfp4_adamw_moments")
-        return m, v
+            return m, v
+        return run_on(stream, self.device, codes, call)

@@ -20,7 +20,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 from . import nvfp4 as N
-from .launch import check, dtype_code, on_stream, ptr
+from .launch import check, dtype_code, new_like, ptr, run_on
 
 
 @dataclass
@@ -32,15 +32,16 @@ class GatedScanGrads:
 
 
 def _sequence(name, t, like):
-    if t.dim() != 3 or t.shape != like.shape:
+    if t.shape != like.shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
                                                            tuple(like.shape)))
-    if t.dtype != like.dtype:
+    if t.dtype is not like.dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
     if t.device != like.device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
     batch, time, chan = t.shape
-    if t.numel() and ((chan > 1 and t.stride(2) != 1) or (time > 1 and t.stride(1) < chan)):
+    if not t.is_contiguous() and t.numel() and (
+            (chan > 1 and t.stride(2) != 1) or (time > 1 and t.stride(1) < chan)):
         raise ValueError("%s must have unit channel stride and time steps apart" % name)
 
 
@@ -67,7 +68,8 @@ def _check_inputs(g, u, floor, h0, reset):
 
 def _strides(t):
     batch, time, _ = t.shape
-    return (t.stride(0) if batch > 1 else 0), (t.stride(1) if time > 1 else 0)
+    b, t, _ = t.stride()
+    return (b if batch > 1 else 0), (t if time > 1 else 0)
 
 
 def _args(g, u, floor, h0, reset, y, h_last):
@@ -84,14 +86,20 @@ def gated_scan_forward(g, u, floor=None, h0=None, reset=None, h_last=None, strea
     _check_inputs(g, u, floor, h0, reset)
     batch, time, chan = g.shape
     _state("h_last", h_last, (batch, chan), g)
-    with on_stream(stream, g.device, (g, u, floor, h0, reset, h_last)) as handle:
-        y = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-        if h_last is None:
-            h_last = torch.empty((batch, chan), dtype=torch.float32, device=g.device)
+    dev, given = g.device, h_last
+
+    def call(handle):
+        y = new_like(g)
+        last = given if given is not None else (
+            torch.empty((batch, chan), dtype=torch.float32, device=dev))
         need = N.nvfp4_gated_scan_workspace_bytes(batch, time, chan, 0)
-        ws = torch.empty(need, dtype=torch.uint8, device=g.device)
-        check(N.nvfp4_gated_scan_forward(_args(g, u, floor, h0, reset, y, h_last), ptr(ws), need,
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        check(N.nvfp4_gated_scan_forward(_args(g, u, floor, h0, reset, y, last), ptr(ws), need,
                                          handle), "nvfp4_gated_scan_forward")
+        return y, last
+    y, h_last = run_on(stream, dev, (g, u, floor, h0, reset, given), call)
+    if given is not None:
+        torch.autograd.graph.increment_version(given)
     return y, h_last
 
 
@@ -105,19 +113,21 @@ def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=No
     _sequence("y", y, g)
     batch, time, chan = g.shape
     _state("dh_last", dh_last, (batch, chan), g)
-    with on_stream(stream, g.device, (dy, g, u, y, floor, h0, reset, dh_last)) as handle:
-        dev = g.device
-        dg = torch.empty(g.shape, dtype=g.dtype, device=dev)
-        du = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    dev = g.device
+
+    def call(handle):
+        dg = new_like(g)
+        du = new_like(g)
         dh0 = torch.empty((batch, chan), dtype=torch.float32, device=dev)
-        dfloor = None if floor is None else torch.empty(chan, dtype=torch.float32, device=dev)
+        dfloor = None if floor is None else torch.empty_like(floor)
         need = N.nvfp4_gated_scan_workspace_bytes(batch, time, chan, 1)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         grads = N.ScanGradArgs(ptr(dy), *_strides(dy), ptr(dh_last), ptr(dg), *_strides(dg),
                                ptr(du), *_strides(du), ptr(dh0), ptr(dfloor))
         check(N.nvfp4_gated_scan_backward(_args(g, u, floor, h0, reset, y, None), grads, ptr(ws),
                                           need, handle), "nvfp4_gated_scan_backward")
-    return GatedScanGrads(dg, du, dh0, dfloor)
+        return GatedScanGrads(dg, du, dh0, dfloor)
+    return run_on(stream, dev, (dy, g, u, y, floor, h0, reset, dh_last), call)
 
 
 _AUTOGRAD = {}
