@@ -177,12 +177,41 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[16][N], int
   turn ^= 1;
 }
 
+// ---------------------------------------------------------------- columns of a thread
+// Where a thread's 8 columns are.  Rows of 8 columns or more: the last threads of a row take
+// its last 8 elements, so that no load depends on a branch; their own are the elements
+// own .. 7 (none for a thread past the end), and the weights of the others are zero, which
+// keeps them out of every sum.  PART (fewer than 8 columns): cnt elements exist.
+template <bool PART>
+struct Place {
+  int col, own, cnt;
+  __device__ __forceinline__ Place(int at, int cols) : col(at), own(0), cnt(8) {
+    if constexpr (PART) {
+      cnt = cols - at;
+    } else if (at > cols - 8) {
+      own = min(8, at - (cols - 8));
+      col = cols - 8;
+    }
+  }
+};
+
+template <bool PART, bool F32>
+__device__ __forceinline__ void fetch(const void *p, int64_t i, int cnt, Raw<F32> &r) {
+  if constexpr (PART) {
+    r.zero();
+    r.load(p, i, cnt);
+  } else {
+    r.load8(p, i);
+  }
+}
+
 // ---------------------------------------------------------------- forward
 // blockDim = (64 waves, rows at a time); rows at a time is 1 unless waves is 1.  HOLD: the
 // weights (and a gate shared by all rows) stay in registers and the next row is fetched
-// ahead; rows of more than 16384 columns leave no registers for either.
-template <bool XF, bool ZF, int K, bool HOLD>
-__global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
+// ahead; rows of more than 16384 columns leave no registers for either.  THREADS bounds the
+// workgroup.
+template <bool XF, bool ZF, int K, bool HOLD, int THREADS, bool PART>
+__global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormForward n) {
   __shared__ float part[2][16][1];
   const nvfp4_norm_params &p = n.p;
   const nvfp4_norm_forward_args &a = n.a;
@@ -194,12 +223,25 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
   const float scale = 1.0f / (float)cols;
   int turn = 0;
 
-  int col[K], cnt[K];
+  int col[K], own[K], cnt[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    col[k] = (k * (int)blockDim.x + tid) * 8;
-    cnt[k] = cols - col[k];
+    const Place<PART> at((k * (int)blockDim.x + tid) * 8, cols);
+    col[k] = at.col;
+    own[k] = at.own;
+    cnt[k] = at.cnt;
   }
+  // sum of squares of the thread's own elements
+  auto squares = [&](int k, float sum, auto &&value) {
+    if (own[k] == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(value(j), value(j), sum);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = j < own[k] ? sum : __builtin_fmaf(value(j), value(j), sum);
+    }
+    return sum;
+  };
   // (c + post) branch [gate], and c + next
   float wp[HOLD ? K : 1][8], wn[HOLD ? K : 1][8];
   auto post_of = [&](int k, float (&w)[8]) {
@@ -227,19 +269,18 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
 
   Raw<XF> rx[K];
   Raw<ZF> rz[K];
-  auto fetch = [&](int64_t row) {
+  auto fetch_x_z = [&](int64_t row) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      rx[k].zero();
       rz[k].zero();
-      rx[k].load(a.x, row * a.ld_x + col[k], cnt[k]);
-      if (branch) rz[k].load(a.z, row * a.ld_z + col[k], cnt[k]);
+      fetch<PART>(a.x, row * a.ld_x + col[k], cnt[k], rx[k]);
+      if (branch) fetch<PART>(a.z, row * a.ld_z + col[k], cnt[k], rz[k]);
     }
   };
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (HOLD && row < rows) fetch(row);
+  if (HOLD && row < rows) fetch_x_z(row);
   for (; row < rows; row += step) {
-    if (!HOLD) fetch(row);
+    if (!HOLD) fetch_x_z(row);
     float x[K][8];
     Raw<ZF> z[K];
 #pragma unroll
@@ -248,13 +289,11 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[k][j] = rx[k].get(j);
     }
-    if (HOLD && row + step < rows) fetch(row + step);
+    if (HOLD && row + step < rows) fetch_x_z(row + step);
     if (branch) {
       float s[1] = {0.0f};
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += z[k].get(j) * z[k].get(j);
+      for (int k = 0; k < K; ++k) s[0] = squares(k, s[0], [&](int j) { return z[k].get(j); });
       row_sum<1>(s, part, turn, waves);
       const float rp = 1.0f / sqrtf(s[0] * scale + p.eps);
       if (tid == 0) a.rstd_post[row] = rp;
@@ -275,16 +314,14 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          x[k][j] = rounded<XF>(p.skip_scale * x[k][j] + z[k].get(j) * rp * w[j]);
-        store<XF>(a.x_out, row * a.ld_x_out + col[k], cnt[k], x[k]);
+          x[k][j] = rounded<XF>(__builtin_fmaf(z[k].get(j) * rp, w[j], p.skip_scale * x[k][j]));
+        if (own[k] < 8) store<XF>(a.x_out, row * a.ld_x_out + col[k], cnt[k], x[k], own[k]);
       }
     }
     if (!next) continue;
     float s[1] = {0.0f};
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += x[k][j] * x[k][j];
+    for (int k = 0; k < K; ++k) s[0] = squares(k, s[0], [&](int j) { return x[k][j]; });
     row_sum<1>(s, part, turn, waves);
     const float r = 1.0f / sqrtf(s[0] * scale + p.eps);
     if (tid == 0) a.rstd[row] = r;
@@ -299,7 +336,7 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormForward n) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = x[k][j] * r * w[j];
-      store<ZF>(a.h, row * a.ld_h + col[k], cnt[k], w);
+      if (own[k] < 8) store<ZF>(a.h, row * a.ld_h + col[k], cnt[k], w, own[k]);
     }
   }
 }
@@ -349,23 +386,6 @@ __device__ __forceinline__ void slot_rows(const Split &s, int64_t slot, int64_t 
   }
 }
 
-// Where a thread's 8 columns are.  Rows of 8 columns or more: the last threads of a row take
-// its last 8 elements, so that no load depends on a branch; their own are the elements
-// own .. 7 (none for a thread past the end), and the weights of the others are zero, which
-// keeps them out of every sum.  PART (fewer than 8 columns): cnt elements exist.
-template <bool PART>
-struct Place {
-  int col, own, cnt;
-  __device__ __forceinline__ Place(int at, int cols) : col(at), own(0), cnt(8) {
-    if constexpr (PART) {
-      cnt = cols - at;
-    } else if (at > cols - 8) {
-      own = min(8, at - (cols - 8));
-      col = cols - 8;
-    }
-  }
-};
-
 // What a thread keeps for its columns: c + next; G = branch gate (c + post) of the current
 // group; and the sums over rows.
 struct Columns {
@@ -382,16 +402,6 @@ struct Operands {         // one row's
 // Workgroups' sums in the workspace: [dnext, dpost, dgate][workgroup][column].
 __device__ __forceinline__ float *sums_at(void *ws, const Split &s, int which, int64_t wg, int cols) {
   return static_cast<float *>(ws) + ((int64_t)which * s.sums + wg) * cols;
-}
-
-template <bool PART, bool F32>
-__device__ __forceinline__ void fetch(const void *p, int64_t i, int cnt, Raw<F32> &r) {
-  if constexpr (PART) {
-    r.zero();
-    r.load(p, i, cnt);
-  } else {
-    r.load8(p, i);
-  }
 }
 
 template <bool PART, bool XF, bool ZF>
@@ -461,36 +471,41 @@ __device__ __forceinline__ void close_group(const NormBackward &b, const Split &
   }
 }
 
-// A thread's share of the three row sums.
+// A thread's share of three sums over a row: t x, G z (dx_out + rstd t) and G z x with
+// t = dh (c + next); their factors rstd and rstd_post are the row's.
 template <bool XF, bool ZF>
 __device__ __forceinline__ void partial_sums(const Operands<XF, ZF> &o, const Columns &c, float r,
-                                             float rp, float (&s)[3]) {
+                                             float (&s)[3]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float n = o.x.get(j) * r, t = o.h.get(j) * c.wn[j];
-    const float q = c.g[j] * (o.z.get(j) * rp);
-    s[0] += t * n;
-    s[1] += q * (o.d.get(j) + r * t);
-    s[2] += q * n;
+    const float x = o.x.get(j), t = o.h.get(j) * c.wn[j], q = c.g[j] * o.z.get(j);
+    s[0] = __builtin_fmaf(t, x, s[0]);
+    s[1] = __builtin_fmaf(q, __builtin_fmaf(r, t, o.d.get(j)), s[1]);
+    s[2] = __builtin_fmaf(q, x, s[2]);
   }
 }
 
-// dx and dz of one row, and its terms of the sums over rows.  m1 = mean(t n) and
-// m2 = mean(G D n2).
+// The row's means m1 = mean(t n) and m2 = mean(G D n2) from those sums.
+__device__ __forceinline__ void means_of(const float (&s)[3], float r, float rp, float scale, float &m1, float &m2) {
+  m1 = r * s[0] * scale;
+  m2 = rp * (s[1] - r * r * m1 * s[2]) * scale;
+}
+
+// dx and dz of one row, and its terms of the sums over rows.
 template <bool PART, bool XF, bool ZF>
 __device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, const Operands<XF, ZF> &o,
                                            const Place<PART> &at, float r, float rp, float m1, float m2,
                                            Columns &c) {
-  const float skip = b.a.z ? b.p.skip_scale : 1.0f;
+  const float skip = b.a.z ? b.p.skip_scale : 1.0f, k1 = -r * m1, k2 = -rp * m2;
   float dx[8], dz[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float n = o.x.get(j) * r, dh = o.h.get(j), n2 = o.z.get(j) * rp;
-    const float d = o.d.get(j) + r * (dh * c.wn[j] - n * m1);
-    c.next[j] += dh * n;
-    c.s[j] += d * n2;
+    const float x = o.x.get(j), dh = o.h.get(j), n2 = o.z.get(j) * rp;
+    const float d = __builtin_fmaf(r, __builtin_fmaf(x, k1, dh * c.wn[j]), o.d.get(j));
+    c.next[j] = __builtin_fmaf(dh, x * r, c.next[j]);
+    c.s[j] = __builtin_fmaf(d, n2, c.s[j]);
     dx[j] = skip * d;
-    dz[j] = rp * (c.g[j] * d - n2 * m2);
+    dz[j] = __builtin_fmaf(c.g[j] * d, rp, n2 * k2);
   }
   if (at.own >= 8) return;
   store<XF>(b.a.dx, row * b.a.ld_dx + at.col, at.cnt, dx, at.own);
@@ -576,9 +591,10 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, 
   walk_rows<kAhead, PART, XF, ZF>(b, sp, row, end, count, at, c, [&](int64_t i, bool live, const Operands<XF, ZF> &o) {
     const float r = b.a.next_weight ? b.a.rstd[i] : 0.0f, rp = b.a.z ? b.a.rstd_post[i] : 0.0f;
     float s[3] = {0.0f, 0.0f, 0.0f};
-    partial_sums(o, c, r, rp, s);
+    partial_sums(o, c, r, s);
     row_sum<3>(s, part, turn, waves);
-    const float m1 = s[0] * scale, m2 = (s[1] - r * m1 * s[2]) * scale;
+    float m1, m2;
+    means_of(s, r, rp, scale, m1, m2);
     if (live) finish_row(b, i, o, at, r, rp, m1, m2, c);
   });
   close_slots(b, sp, blockIdx.x, at, c, lds);
@@ -601,14 +617,10 @@ __global__ __launch_bounds__(512) void norm_means_kernel(NormBackward b, float *
       fetch_row(b.a, row, at, o);
       Columns c;
       open_slot(b, row / per, at, c);
-      partial_sums(o, c, r, rp, s);
+      partial_sums(o, c, r, s);
     }
     row_sum<3>(s, part, turn, waves);
-    const float m1 = s[0] * scale;
-    if (threadIdx.x == 0) {
-      means[2 * row] = m1;
-      means[2 * row + 1] = (s[1] - r * m1 * s[2]) * scale;
-    }
+    if (threadIdx.x == 0) means_of(s, r, rp, scale, means[2 * row], means[2 * row + 1]);
   }
 }
 
@@ -684,21 +696,24 @@ Split split_of(const nvfp4_norm_params &p) {
   return split_rows(p.rows, p.gate_rows, streams, kCus);
 }
 
-template <bool XF, bool ZF, int K, bool HOLD>
+template <bool XF, bool ZF, int K, bool HOLD, int THREADS, bool PART = false>
 hipError_t run_forward(const NormForward &n, hipStream_t stream) {
   const int waves = waves_of(n.p.cols, 8 * K), y = waves == 1 ? 4 : 1;
   const int64_t want = (n.p.rows + y - 1) / y, most = (int64_t)kCus * 2 * resident(64 * waves * y);
-  norm_forward_kernel<XF, ZF, K, HOLD>
+  norm_forward_kernel<XF, ZF, K, HOLD, THREADS, PART>
       <<<(uint32_t)(want < most ? want : most), dim3(64 * waves, y), 0, stream>>>(n);
   return hipGetLastError();
 }
 
 template <bool XF, bool ZF>
 hipError_t forward_of(const NormForward &n, hipStream_t stream) {
-  // as few elements per thread as 1024 threads allow
-  if (n.p.cols <= 8192) return run_forward<XF, ZF, 1, true>(n, stream);
-  if (n.p.cols <= 16384) return run_forward<XF, ZF, 2, true>(n, stream);
-  return run_forward<XF, ZF, 4, false>(n, stream);
+  // as few elements per thread as the workgroup's threads allow
+  const int64_t cols = n.p.cols;
+  if (cols < 8) return run_forward<XF, ZF, 1, true, 1024, true>(n, stream);
+  if (cols <= 8192) return run_forward<XF, ZF, 1, true, 1024>(n, stream);
+  if (cols <= 16384) return run_forward<XF, ZF, 2, true, 1024>(n, stream);
+  if (cols <= 20480) return run_forward<XF, ZF, 4, false, 640>(n, stream);
+  return run_forward<XF, ZF, 4, false, 1024>(n, stream);
 }
 
 template <bool XF, bool ZF>
