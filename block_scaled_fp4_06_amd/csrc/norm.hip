@@ -138,6 +138,10 @@ __device__ __forceinline__ void store_param(void *p, int f32, int64_t i, float v
   else static_cast<uint16_t *>(p)[i] = bf16_bits_rn(v);
 }
 
+// threadIdx.y of a wave's lanes, which all have the same: the rows that follow from it, and
+// their addresses, are then kept once per wave.
+__device__ __forceinline__ int wave_y() { return (int)__builtin_amdgcn_readfirstlane(threadIdx.y); }
+
 // ---------------------------------------------------------------- sums over a row
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_add(float v) {
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormForward n) {
       if (branch) fetch<PART>(a.z, row * a.ld_z + col[k], cnt[k], rz[k]);
     }
   };
-  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + wave_y();
   if (HOLD && row < rows) fetch_x_z(row);
   for (; row < rows; row += step) {
     if (!HOLD) fetch_x_z(row);
@@ -397,6 +401,14 @@ template <bool XF, bool ZF>
 struct Operands {         // one row's
   Raw<XF> x, d;
   Raw<ZF> z, h;
+  // Makes the compiler unpack the words again where they are used next, instead of keeping
+  // 32 unpacked values across the row's reduction.
+  __device__ __forceinline__ void unpack_again() {
+#pragma unroll
+    for (int i = 0; i < Raw<XF>::kWords; ++i) asm volatile("" : "+v"(x.w[i]), "+v"(d.w[i]));
+#pragma unroll
+    for (int i = 0; i < Raw<ZF>::kWords; ++i) asm volatile("" : "+v"(z.w[i]), "+v"(h.w[i]));
+  }
 };
 
 // Workgroups' sums in the workspace: [dnext, dpost, dgate][workgroup][column].
@@ -512,25 +524,35 @@ __device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, c
   if (b.a.z) store<ZF>(b.a.dz, row * b.a.ld_dz + at.col, at.cnt, dz, at.own);
 }
 
-// Walks over `count` rows from `row` on (do_row for each that is before `end`: the streams
-// of a workgroup take the same number of turns), AHEAD rows' operands in flight, and the
-// groups' ends between them.
-template <int AHEAD, bool PART, bool XF, bool ZF, class Row>
+// Walks over `count` rows from `row` on, R at a time (do_rows: the first one's index, which
+// of them are before `end`, their operands; the streams of a workgroup take the same number
+// of turns), the next R rows' operands in flight, and the groups' ends between them.  ONE:
+// all rows are of one group, so nothing but s is kept for dpost and dgate along the way;
+// otherwise R is 1.
+template <int R, bool ONE, bool PART, bool XF, bool ZF, class Rows>
 __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp, int64_t row, int64_t end,
-                                          int64_t count, const Place<PART> &at, Columns &c, Row &&do_row) {
+                                          int64_t count, const Place<PART> &at, Columns &c, Rows &&do_rows) {
+  static_assert(ONE || R == 1, "groups may end after any row");
   const int64_t per = sp.rows / sp.groups, last = max((int64_t)0, min(end, sp.rows) - 1);
   int64_t group = min(row, last) / per, left = (group + 1) * per - row;   // rows of the group from here on
   open_slot(b, group, at, c);
-  Operands<XF, ZF> o, ahead[AHEAD];
+  Operands<XF, ZF> o[R], ahead[R];
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) fetch_row<PART>(b.a, min(row + k, last), at, ahead[k]);
-  for (int64_t i = 0; i < count; ++i, ++row) {
-    o = ahead[0];
+  for (int k = 0; k < R; ++k) fetch_row<PART>(b.a, min(row + k, last), at, ahead[k]);
+  for (int64_t i = 0; i < count; i += R, row += R) {
+    int64_t rows[R];
+    bool live[R];
 #pragma unroll
-    for (int k = 0; k + 1 < AHEAD; ++k) ahead[k] = ahead[k + 1];
-    if (i + AHEAD < count) fetch_row<PART>(b.a, min(row + AHEAD, last), at, ahead[AHEAD - 1]);
-    do_row(min(row, last), row < end, o);
-    if (row < end && (--left == 0 || row + 1 == end)) {
+    for (int k = 0; k < R; ++k) {
+      o[k] = ahead[k];
+      rows[k] = min(row + k, last);
+      live[k] = row + k < end;
+    }
+    if (i + R < count)
+#pragma unroll
+      for (int k = 0; k < R; ++k) fetch_row<PART>(b.a, min(row + R + k, last), at, ahead[k]);
+    do_rows(rows, live, o);
+    if (!ONE && row < end && (--left == 0 || row + 1 == end)) {
       close_group(b, sp, group, at, c);
       if (row + 1 < end) {
         open_group(b, ++group, at, c);
@@ -538,6 +560,7 @@ __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp
       }
     }
   }
+  if (ONE) close_group(b, sp, group, at, c);
 }
 
 // The sums of a workgroup's streams, added in order through LDS, into the workspace.  (A
@@ -565,14 +588,14 @@ __device__ __forceinline__ void close_slots(const NormBackward &b, const Split &
   }
 }
 
-// blockDim = (64 waves, streams): a row per stream at a time.  THREADS bounds the workgroup:
-// fewer threads leave more registers to each.
-template <bool XF, bool ZF, int THREADS, bool PART>
+// blockDim = (64 waves, streams): R rows per stream at a time, whose sums share one
+// reduction.  THREADS bounds the workgroup: fewer threads leave more registers to each.
+template <bool XF, bool ZF, int THREADS, int R, bool ONE, bool PART>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, Split sp) {
-  __shared__ float part[2][16][3];
+  __shared__ float part[2][16][3 * R];
   extern __shared__ float lds[];
   const int cols = (int)b.p.cols, waves = blockDim.x >> 6, streams = blockDim.y;
-  const int64_t slot = (int64_t)blockIdx.x * streams + threadIdx.y;
+  const int64_t slot = (int64_t)blockIdx.x * streams + wave_y();
   const float scale = 1.0f / (float)cols;
   const Place<PART> at((int)threadIdx.x * 8, cols);
   int turn = 0;
@@ -586,16 +609,27 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, 
       count = max(count, r1 - r0);
     }
   Columns c;
-  // (binary32 rows, and workgroups of over 640 threads, leave registers for one row ahead)
-  constexpr int kAhead = !XF && !ZF && THREADS <= 640 ? 2 : 1;
-  walk_rows<kAhead, PART, XF, ZF>(b, sp, row, end, count, at, c, [&](int64_t i, bool live, const Operands<XF, ZF> &o) {
-    const float r = b.a.next_weight ? b.a.rstd[i] : 0.0f, rp = b.a.z ? b.a.rstd_post[i] : 0.0f;
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    partial_sums(o, c, r, s);
-    row_sum<3>(s, part, turn, waves);
-    float m1, m2;
-    means_of(s, r, rp, scale, m1, m2);
-    if (live) finish_row(b, i, o, at, r, rp, m1, m2, c);
+  walk_rows<R, ONE, PART, XF, ZF>(b, sp, row, end, count, at, c,
+                                  [&](const int64_t (&rows)[R], const bool (&live)[R], Operands<XF, ZF> (&o)[R]) {
+    float r[R], rp[R], s[3 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      r[k] = b.a.next_weight ? b.a.rstd[rows[k]] : 0.0f;
+      rp[k] = b.a.z ? b.a.rstd_post[rows[k]] : 0.0f;
+      float t[3] = {0.0f, 0.0f, 0.0f};
+      partial_sums(o[k], c, r[k], t);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) s[3 * k + i] = t[i];
+    }
+    row_sum<3 * R>(s, part, turn, waves);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float t[3] = {s[3 * k], s[3 * k + 1], s[3 * k + 2]};
+      float m1, m2;
+      means_of(t, r[k], rp[k], scale, m1, m2);
+      o[k].unpack_again();
+      if (live[k]) finish_row(b, rows[k], o[k], at, r[k], rp[k], m1, m2, c);
+    }
   });
   close_slots(b, sp, blockIdx.x, at, c, lds);
 }
@@ -633,9 +667,11 @@ __global__ __launch_bounds__(256) void norm_strips_kernel(NormBackward b, Split 
   int64_t row, end;
   slot_rows(sp, slot, row, end);
   Columns c;
-  walk_rows<2, false, XF, ZF>(b, sp, row, end, end - row, at, c, [&](int64_t i, bool, const Operands<XF, ZF> &o) {
+  walk_rows<1, false, false, XF, ZF>(b, sp, row, end, end - row, at, c,
+                                     [&](const int64_t (&rows)[1], const bool (&)[1], Operands<XF, ZF> (&o)[1]) {
+    const int64_t i = rows[0];
     const float r = b.a.next_weight ? b.a.rstd[i] : 0.0f, rp = b.a.z ? b.a.rstd_post[i] : 0.0f;
-    finish_row(b, i, o, at, r, rp, means[2 * i], means[2 * i + 1], c);
+    finish_row(b, i, o[0], at, r, rp, means[2 * i], means[2 * i + 1], c);
   });
   close_slots(b, sp, slot, at, c, nullptr);   // (one stream)
 }
@@ -723,9 +759,11 @@ hipError_t backward_of(const NormBackward &b, const Split &sp, hipStream_t strea
     const dim3 block(64 * waves, sp.streams);
     const size_t lds = (size_t)(sp.streams - 1) * 8 * block.x * sizeof(float);
     const uint32_t grid = (uint32_t)sp.sums;
-    if (b.p.cols < 8) norm_backward_kernel<XF, ZF, 640, true><<<grid, block, lds, stream>>>(b, sp);
-    else if (waves <= 10) norm_backward_kernel<XF, ZF, 640, false><<<grid, block, lds, stream>>>(b, sp);
-    else norm_backward_kernel<XF, ZF, 1024, false><<<grid, block, lds, stream>>>(b, sp);
+    const bool one = sp.parts > 0 || sp.groups == 1;
+    if (b.p.cols < 8) norm_backward_kernel<XF, ZF, 640, 1, false, true><<<grid, block, lds, stream>>>(b, sp);
+    else if (waves > 10) norm_backward_kernel<XF, ZF, 1024, 1, false, false><<<grid, block, lds, stream>>>(b, sp);
+    else if (one) norm_backward_kernel<XF, ZF, 640, XF || ZF ? 1 : 2, true, false><<<grid, block, lds, stream>>>(b, sp);
+    else norm_backward_kernel<XF, ZF, 640, 1, false, false><<<grid, block, lds, stream>>>(b, sp);
     return hipGetLastError();
   }
   float *means = static_cast<float *>(b.ws) + 3 * sp.sums * b.p.cols;
