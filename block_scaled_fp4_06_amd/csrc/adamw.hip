@@ -32,66 +32,86 @@ struct GradPointers {
   const void *p[kAdamGrads];
 };
 
-template <int E>
-__device__ __forceinline__ void load_values(const void *p, bool f32, bool wide, int64_t i, int cnt,
-                                            float (&out)[E]) {
-  if (f32) {
-    const float *q = static_cast<const float *>(p) + i;
-    if (wide && cnt == E) {
+// 16 bytes at any element's alignment: a packed type makes them one instruction.
+struct __attribute__((packed, aligned(2))) Four { uint32_t w[4]; };
+struct __attribute__((packed, aligned(2))) Two { uint32_t w[2]; };
+
+// E consecutive values (4 or 8), all there.
+template <bool F32, int E>
+__device__ __forceinline__ void load_whole(const void *p, int64_t i, float (&out)[E]) {
+  if constexpr (F32) {
 #pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(q + j);
-        out[j] = v.x; out[j + 1] = v.y; out[j + 2] = v.z; out[j + 3] = v.w;
-      }
-    } else {
+    for (int j = 0; j < E; j += 4) {
+      const Four v = *reinterpret_cast<const Four *>(static_cast<const float *>(p) + i + j);
 #pragma unroll
-      for (int j = 0; j < E; ++j) out[j] = j < cnt ? q[j] : 0.0f;
+      for (int l = 0; l < 4; ++l) out[j + l] = __uint_as_float(v.w[l]);
+    }
+  } else if constexpr (E == 8) {
+    const Four v = *reinterpret_cast<const Four *>(static_cast<const uint16_t *>(p) + i);
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      out[2 * l] = bf16_lo(v.w[l]);
+      out[2 * l + 1] = bf16_hi(v.w[l]);
     }
   } else {
-    const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-    if (wide && cnt == E) {
+    const Two v = *reinterpret_cast<const Two *>(static_cast<const uint16_t *>(p) + i);
 #pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(q + j);
-        out[j] = bf16_lo(v.x); out[j + 1] = bf16_hi(v.x);
-        out[j + 2] = bf16_lo(v.y); out[j + 3] = bf16_hi(v.y);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) out[j] = j < cnt ? __uint_as_float((uint32_t)q[j] << 16) : 0.0f;
+    for (int l = 0; l < 2; ++l) {
+      out[2 * l] = bf16_lo(v.w[l]);
+      out[2 * l + 1] = bf16_hi(v.w[l]);
     }
   }
 }
 
-template <int E>
-__device__ __forceinline__ void store_f32(float *p, bool wide, int64_t i, int cnt,
-                                          const float (&v)[E]) {
-  float *q = p + i;
-  if (wide && cnt == E) {
+template <bool F32, int E>
+__device__ __forceinline__ void load_part(const void *p, int64_t i, int cnt, float (&out)[E]) {
 #pragma unroll
-    for (int j = 0; j < E; j += 4)
-      *reinterpret_cast<float4 *>(q + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (j < cnt) q[j] = v[j];
+  for (int j = 0; j < E; ++j) {
+    out[j] = 0.0f;
+    if (j >= cnt) continue;
+    if constexpr (F32) out[j] = static_cast<const float *>(p)[i + j];
+    else out[j] = __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i + j] << 16);
   }
 }
 
-template <int E>
-__device__ __forceinline__ void store_u16(uint16_t *p, bool wide, int64_t i, int cnt,
-                                          const uint16_t (&v)[E]) {
-  uint16_t *q = p + i;
-  if (wide && cnt == E) {
+// WHOLE: all E are there; otherwise the first cnt.
+template <bool WHOLE, bool F32, int E>
+__device__ __forceinline__ void load_values(const void *p, int64_t i, int cnt, float (&out)[E]) {
+  if constexpr (WHOLE) load_whole<F32, E>(p, i, out);
+  else load_part<F32, E>(p, i, cnt, out);
+}
+
+template <bool WHOLE, int E>
+__device__ __forceinline__ void store_f32(float *p, int64_t i, int cnt, const float (&v)[E]) {
+  if constexpr (WHOLE) {
 #pragma unroll
     for (int j = 0; j < E; j += 4)
-      *reinterpret_cast<uint2 *>(q + j) = make_uint2((uint32_t)v[j] | ((uint32_t)v[j + 1] << 16),
-                                                     (uint32_t)v[j + 2] | ((uint32_t)v[j + 3] << 16));
+      *reinterpret_cast<Four *>(p + i + j) = Four{{__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                                                   __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])}};
   } else {
 #pragma unroll
     for (int j = 0; j < E; ++j)
-      if (j < cnt) q[j] = v[j];
+      if (j < cnt) p[i + j] = v[j];
   }
+}
+
+// w: pairs of 16-bit values.
+template <bool WHOLE, int E>
+__device__ __forceinline__ void store_u16(uint16_t *p, int64_t i, int cnt, const uint32_t (&w)[E / 2]) {
+  if constexpr (WHOLE) {
+    if constexpr (E == 8) *reinterpret_cast<Four *>(p + i) = Four{{w[0], w[1], w[2], w[3]}};
+    else *reinterpret_cast<Two *>(p + i) = Two{{w[0], w[1]}};
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (j < cnt) p[i + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+// Two bf16 values in a word, nearest-even.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, Pair{(__bf16)lo, (__bf16)hi});
 }
 
 __device__ __forceinline__ bool finite_bits(float v) {
@@ -140,61 +160,52 @@ __device__ __forceinline__ uint32_t root_encode(float t, uint32_t draw) {
   return t > 0.0f ? min(max(c, 1u), 254u) : 0u;
 }
 
-template <int BITS>
-__global__ __launch_bounds__(256) void adamw_kernel(const uint8_t *__restrict__ table, int t0,
-                                                    int t1, int64_t chunk0, AdamScalars s,
-                                                    GradPointers grads) {
-  constexpr int E = BITS == 8 ? 8 : 4;
-  const AdamRow *rows = reinterpret_cast<const AdamRow *>(table + sizeof(AdamHeader));
-  const int64_t chunk = chunk0 + blockIdx.x;
-  int lo = t0, hi = t1;   // the last tensor whose first chunk is at most `chunk`
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (rows[mid].first_chunk <= chunk) lo = mid; else hi = mid;
-  }
-  const nvfp4_adamw_tensor &t = rows[lo].t;
-  const void *g = grads.p[lo - t0];
-  if (!g) return;
-  const int64_t n = t.n;
-  const bool pf = t.param_dtype == NVFP4_DT_FP32, gf = t.grad_dtype == NVFP4_DT_FP32;
-  void *const param = t.param;
-  float *const master = t.master;
-  const bool pwide = ((uintptr_t)param & 15) == 0, gwide = ((uintptr_t)g & 15) == 0,
-             mwide = ((uintptr_t)master & 15) == 0;
-  const float keep = (float)(1.0 - s.lr * t.weight_decay);
-  const float gs = s.grad_scale ? *s.grad_scale : 1.0f;
-  const int64_t begin = (chunk - rows[lo].first_chunk) * kAdamChunk;
-  const int64_t end = min(n, begin + kAdamChunk);
+// What a chunk's elements need of their tensor.
+struct Chunk {
+  const nvfp4_adamw_tensor *t;
+  const void *g;
+  uint32_t tensor;
+  int64_t begin, end;
+  float keep, gs;
+};
 
-  for (int64_t i0 = begin + (threadIdx.x & ~63) * E; i0 < end; i0 += 256 * E) {
+// The elements begin .. end - 1.  WHOLE: they are a whole chunk; otherwise every access is
+// bounded element by element.
+template <int BITS, bool PF, bool MASTER, bool GF, bool WHOLE>
+__device__ __forceinline__ void update(const Chunk &ch, const AdamScalars &s) {
+  constexpr int E = BITS == 8 ? 8 : 4;
+  const nvfp4_adamw_tensor &t = *ch.t;
+  void *const param = t.param, *const exp_avg = t.exp_avg, *const exp_avg_sq = t.exp_avg_sq;
+  float *const master = t.master, *const scale_m = t.exp_avg_scale, *const scale_r = t.exp_avg_sq_scale;
+  for (int64_t i0 = ch.begin + (threadIdx.x & ~63) * E; i0 < ch.end; i0 += 256 * E) {
     const int64_t i = i0 + (threadIdx.x & 63) * E;
-    const int cnt = (int)max((int64_t)0, min((int64_t)E, end - i));
-    float gv[E], w[E], m[E], v[E], r[E];
-    load_values<E>(g, gf, gwide, i, cnt, gv);
-    if (master) load_values<E>(master, true, mwide, i, cnt, w);
-    else load_values<E>(param, pf, pwide, i, cnt, w);
+    const int cnt = WHOLE ? E : (int)max((int64_t)0, min((int64_t)E, ch.end - i));
+    float g[E], w[E], m[E], v[E], r[E];
+    load_values<WHOLE, GF, E>(ch.g, i, cnt, g);
+    if constexpr (MASTER) load_values<WHOLE, true, E>(master, i, cnt, w);
+    else load_values<WHOLE, PF, E>(param, i, cnt, w);
     if constexpr (BITS == 32) {
-      load_values<E>(t.exp_avg, true, true, i, cnt, m);
-      load_values<E>(t.exp_avg_sq, true, true, i, cnt, v);
+      load_values<WHOLE, true, E>(exp_avg, i, cnt, m);
+      load_values<WHOLE, true, E>(exp_avg_sq, i, cnt, v);
     } else {
+      const uint8_t *pm = static_cast<const uint8_t *>(exp_avg) + i, *pv = static_cast<const uint8_t *>(exp_avg_sq) + i;
       uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
       float ms = 0.0f, vs = 0.0f;
-      if (cnt == E) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.exp_avg) + i);
-        const uint2 b = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.exp_avg_sq) + i);
+      if constexpr (WHOLE) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(pm), b = *reinterpret_cast<const uint2 *>(pv);
         mc[0] = a.x; mc[1] = a.y;
         vc[0] = b.x; vc[1] = b.y;
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j)
           if (j < cnt) {
-            mc[j >> 2] |= (uint32_t) static_cast<const uint8_t *>(t.exp_avg)[i + j] << (8 * (j & 3));
-            vc[j >> 2] |= (uint32_t) static_cast<const uint8_t *>(t.exp_avg_sq)[i + j] << (8 * (j & 3));
+            mc[j >> 2] |= (uint32_t)pm[j] << (8 * (j & 3));
+            vc[j >> 2] |= (uint32_t)pv[j] << (8 * (j & 3));
           }
       }
-      if (cnt > 0) {
-        ms = t.exp_avg_scale[i / NVFP4_ADAMW_BLOCK];
-        vs = t.exp_avg_sq_scale[i / NVFP4_ADAMW_BLOCK];
+      if (WHOLE || cnt > 0) {
+        ms = scale_m[i / NVFP4_ADAMW_BLOCK];
+        vs = scale_r[i / NVFP4_ADAMW_BLOCK];
       }
 #pragma unroll
       for (int j = 0; j < E; ++j) {
@@ -205,54 +216,84 @@ __global__ __launch_bounds__(256) void adamw_kernel(const uint8_t *__restrict__ 
     }
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float gj = s.grad_scale ? gv[j] * gs : gv[j];
+      const float gj = s.grad_scale ? g[j] * ch.gs : g[j];
       m[j] = s.beta1 * m[j] + s.omb1 * gj;
       v[j] = s.beta2 * v[j] + s.omb2 * (gj * gj);
       r[j] = sqrtf(v[j]);
-      w[j] = w[j] * keep - s.rate * (m[j] / (r[j] * s.root + s.eps));
+      w[j] = w[j] * ch.keep - s.rate * (m[j] / (r[j] * s.root + s.eps));
     }
-    if (master) store_f32<E>(master, mwide, i, cnt, w);
-    if (pf) {
-      store_f32<E>(static_cast<float *>(param), pwide, i, cnt, w);
+    if constexpr (MASTER) store_f32<WHOLE, E>(master, i, cnt, w);
+    if constexpr (PF) {
+      store_f32<WHOLE, E>(static_cast<float *>(param), i, cnt, w);
     } else {
-      uint16_t b[E];
+      uint32_t b[E / 2];
       if (s.stochastic_param) {
-        const Philox4 d = draws8(i >> 3, s, (uint32_t)lo, 1u);
+        const Philox4 d = draws8(i >> 3, s, ch.tensor, 1u);
+        // (E = 4: the lanes of the upper half of eight take the last two words)
+        const uint32_t words[4] = {E == 4 && (i & 4) ? d.z : d.x, E == 4 && (i & 4) ? d.w : d.y, d.z, d.w};
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const uint32_t bits = __float_as_uint(w[j]) + lane_draw(d, (E == 8 ? 0 : (int)(i & 4)) + j);
-          b[j] = finite_bits(w[j]) ? (uint16_t)(bits >> 16) : bf16_bits_rn(w[j]);
+        for (int j = 0; j < E / 2; ++j) {
+          const float a = w[2 * j], c = w[2 * j + 1];
+          const uint32_t lo = __float_as_uint(a) + (words[j] & 0xFFFFu), hi = __float_as_uint(c) + (words[j] >> 16);
+          b[j] = (lo >> 16) | (hi & 0xFFFF0000u);
+          if (!finite_bits(a) || !finite_bits(c)) {   // inf and NaN take no draw
+            const uint32_t n = pack2(a, c);
+            if (!finite_bits(a)) b[j] = (b[j] & 0xFFFF0000u) | (n & 0xFFFFu);
+            if (!finite_bits(c)) b[j] = (b[j] & 0xFFFFu) | (n & 0xFFFF0000u);
+          }
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j) b[j] = bf16_bits_rn(w[j]);
+        for (int j = 0; j < E / 2; ++j) b[j] = pack2(w[2 * j], w[2 * j + 1]);
       }
-      store_u16<E>(static_cast<uint16_t *>(param), pwide, i, cnt, b);
+      store_u16<WHOLE, E>(static_cast<uint16_t *>(param), i, cnt, b);
     }
     if constexpr (BITS == 32) {
-      store_f32<E>(static_cast<float *>(t.exp_avg), true, i, cnt, m);
-      store_f32<E>(static_cast<float *>(t.exp_avg_sq), true, i, cnt, v);
+      store_f32<WHOLE, E>(static_cast<float *>(exp_avg), i, cnt, m);
+      store_f32<WHOLE, E>(static_cast<float *>(exp_avg_sq), i, cnt, v);
     } else {
       uint32_t topm = 0u, topr = 0u;
+      bool odd = false;   // a moment that is not finite
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        if (j < cnt && finite_bits(m[j])) topm = max(topm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-        if (j < cnt && finite_bits(r[j])) topr = max(topr, __float_as_uint(r[j]));
+        if (!WHOLE && j >= cnt) continue;
+        const uint32_t am = __float_as_uint(m[j]) & 0x7FFFFFFFu, ar = __float_as_uint(r[j]) & 0x7FFFFFFFu;
+        odd |= max(am, ar) >= 0x7F800000u;
+        topm = max(topm, am);
+        topr = max(topr, ar);
+      }
+      if (__any(odd)) {   // (they do not enter the block's scale)
+        topm = topr = 0u;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          if (!WHOLE && j >= cnt) continue;
+          if (finite_bits(m[j])) topm = max(topm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+          if (finite_bits(r[j])) topr = max(topr, __float_as_uint(r[j]));
+        }
       }
       const BlockScale bm = block_scale(half_max(topm), kExpM), br = block_scale(half_max(topr), kExpR);
-      const Philox4 d = draws8(i >> 3, s, (uint32_t)lo, 0u);
+      const bool live = bm.scale > 0.0f;
+      const Philox4 d = draws8(i >> 3, s, ch.tensor, 0u);
       uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(bm.scale > 0.0f ? m[j] * bm.inv : 0.0f, 0.0f, 0, false) & 0xFFu;
-        if (!finite_bits(m[j])) c = 0x7Fu;
-        mc[j >> 2] |= c << (8 * (j & 3));
-        c = root_encode(r[j] * br.inv, lane_draw(d, j));
-        if (!finite_bits(r[j])) c = 255u;
-        vc[j >> 2] |= c << (8 * (j & 3));
+      for (int j = 0; j < E; j += 4) {
+        const float a = m[j] * bm.inv, b = m[j + 1] * bm.inv, c = m[j + 2] * bm.inv, e = m[j + 3] * bm.inv;
+        uint32_t q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, e, (int)q, true);
+        mc[j >> 2] = live ? q : 0u;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) vc[j >> 2] |= root_encode(r[j + l] * br.inv, lane_draw(d, j + l)) << (8 * l);
       }
-      uint8_t *pm = static_cast<uint8_t *>(t.exp_avg) + i, *pv = static_cast<uint8_t *>(t.exp_avg_sq) + i;
-      if (cnt == E) {
+      if (__any(odd)) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const uint32_t byte = 0xFFu << (8 * (j & 3));
+          if (!finite_bits(m[j])) mc[j >> 2] = (mc[j >> 2] & ~byte) | (0x7Fu << (8 * (j & 3)));
+          if (!finite_bits(r[j])) vc[j >> 2] |= byte;
+        }
+      }
+      uint8_t *pm = static_cast<uint8_t *>(exp_avg) + i, *pv = static_cast<uint8_t *>(exp_avg_sq) + i;
+      if constexpr (WHOLE) {
         *reinterpret_cast<uint2 *>(pm) = make_uint2(mc[0], mc[1]);
         *reinterpret_cast<uint2 *>(pv) = make_uint2(vc[0], vc[1]);
       } else {
@@ -263,44 +304,103 @@ __global__ __launch_bounds__(256) void adamw_kernel(const uint8_t *__restrict__ 
             pv[j] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
           }
       }
-      if (cnt > 0 && (threadIdx.x & 31) == 0) {
-        t.exp_avg_scale[i / NVFP4_ADAMW_BLOCK] = bm.scale;
-        t.exp_avg_sq_scale[i / NVFP4_ADAMW_BLOCK] = br.scale;
+      if ((WHOLE || cnt > 0) && (threadIdx.x & 31) == 0) {
+        scale_m[i / NVFP4_ADAMW_BLOCK] = bm.scale;
+        scale_r[i / NVFP4_ADAMW_BLOCK] = br.scale;
       }
     }
   }
 }
 
-// One thread per 8 codes of each moment.
+template <int BITS, bool PF, bool MASTER>
+__device__ __forceinline__ void update_as(const Chunk &c, const AdamScalars &s) {
+  const bool whole = c.end - c.begin == kAdamChunk;
+  if (c.t->grad_dtype == NVFP4_DT_FP32) {
+    if (whole) update<BITS, PF, MASTER, true, true>(c, s);
+    else update<BITS, PF, MASTER, true, false>(c, s);
+  } else {
+    if (whole) update<BITS, PF, MASTER, false, true>(c, s);
+    else update<BITS, PF, MASTER, false, false>(c, s);
+  }
+}
+
+template <int BITS>
+__global__ __launch_bounds__(256) void adamw_kernel(const uint8_t *__restrict__ table, int t0, int t1,
+                                                    int64_t chunk0, AdamScalars s, GradPointers grads) {
+  const AdamRow *rows = reinterpret_cast<const AdamRow *>(table + sizeof(AdamHeader));
+  const int64_t chunk = chunk0 + blockIdx.x;
+  int lo = t0, hi = t1;   // the last tensor whose first chunk is at most `chunk`
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (rows[mid].first_chunk <= chunk) lo = mid; else hi = mid;
+  }
+  Chunk c;
+  c.t = &rows[lo].t;
+  c.g = grads.p[lo - t0];
+  if (!c.g) return;
+  c.tensor = (uint32_t)lo;
+  c.begin = (chunk - rows[lo].first_chunk) * kAdamChunk;
+  c.end = min(c.t->n, c.begin + kAdamChunk);
+  c.keep = (float)(1.0 - s.lr * c.t->weight_decay);
+  c.gs = s.grad_scale ? *s.grad_scale : 1.0f;
+  if (c.t->param_dtype == NVFP4_DT_FP32) update_as<BITS, true, false>(c, s);
+  else if (c.t->master) update_as<BITS, false, true>(c, s);
+  else update_as<BITS, false, false>(c, s);
+}
+
+// One thread per 8 codes of each moment (the last thread bounds its accesses).
 template <bool F32>
 __global__ __launch_bounds__(256) void moments_kernel(AdamMoments l) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= l.n) return;
-  const int cnt = (int)min((int64_t)8, l.n - i);
-  const float ms = l.ms[i / NVFP4_ADAMW_BLOCK], vs = l.vs[i / NVFP4_ADAMW_BLOCK];
-  float m[8], v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] = j < cnt ? e4m3_decode(l.m[i + j]) * ms : 0.0f;
-    const float q = j < cnt ? root_decode(l.v[i + j]) * vs : 0.0f;
-    v[j] = q * q;
-  }
-  if constexpr (F32) {
-    store_f32<8>(static_cast<float *>(l.m_out), true, i, cnt, m);
-    store_f32<8>(static_cast<float *>(l.v_out), true, i, cnt, v);
-  } else {
-    uint16_t a[8], b[8];
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < l.n; i += (int64_t)gridDim.x * 2048) {
+    const int cnt = (int)min((int64_t)8, l.n - i);
+    const float ms = l.ms[i / NVFP4_ADAMW_BLOCK], vs = l.vs[i / NVFP4_ADAMW_BLOCK];
+    uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
+    if (cnt == 8) {
+      const uint2 a = *reinterpret_cast<const uint2 *>(l.m + i), b = *reinterpret_cast<const uint2 *>(l.v + i);
+      mc[0] = a.x; mc[1] = a.y;
+      vc[0] = b.x; vc[1] = b.y;
+    } else {
+      for (int j = 0; j < cnt; ++j) {
+        mc[j >> 2] |= (uint32_t)l.m[i + j] << (8 * (j & 3));
+        vc[j >> 2] |= (uint32_t)l.v[i + j] << (8 * (j & 3));
+      }
+    }
+    float m[8], v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      a[j] = bf16_bits_rn(m[j]);
-      b[j] = bf16_bits_rn(v[j]);
+      m[j] = e4m3_decode((mc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * ms;
+      const float q = root_decode((vc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * vs;
+      v[j] = q * q;
     }
-    store_u16<8>(static_cast<uint16_t *>(l.m_out), true, i, cnt, a);
-    store_u16<8>(static_cast<uint16_t *>(l.v_out), true, i, cnt, b);
+    if constexpr (F32) {
+      if (cnt == 8) {
+        store_f32<true, 8>(static_cast<float *>(l.m_out), i, cnt, m);
+        store_f32<true, 8>(static_cast<float *>(l.v_out), i, cnt, v);
+      } else {
+        store_f32<false, 8>(static_cast<float *>(l.m_out), i, cnt, m);
+        store_f32<false, 8>(static_cast<float *>(l.v_out), i, cnt, v);
+      }
+    } else {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = pack2(m[2 * j], m[2 * j + 1]);
+        b[j] = pack2(v[2 * j], v[2 * j + 1]);
+      }
+      if (cnt == 8) {
+        store_u16<true, 8>(static_cast<uint16_t *>(l.m_out), i, cnt, a);
+        store_u16<true, 8>(static_cast<uint16_t *>(l.v_out), i, cnt, b);
+      } else {
+        store_u16<false, 8>(static_cast<uint16_t *>(l.m_out), i, cnt, a);
+        store_u16<false, 8>(static_cast<uint16_t *>(l.v_out), i, cnt, b);
+      }
+    }
   }
 }
 
 }  // namespace
+
+constexpr int64_t kMaxGrid = 1 << 23;
 
 hipError_t launch_adamw(const AdamLaunch &l, hipStream_t stream) {
   const AdamRow *rows = reinterpret_cast<const AdamRow *>(l.host + 1);
@@ -313,18 +413,21 @@ hipError_t launch_adamw(const AdamLaunch &l, hipStream_t stream) {
     GradPointers g;
     for (int64_t i = 0; i < kAdamGrads; ++i) g.p[i] = t0 + i < t1 ? l.grads[t0 + i] : nullptr;
     const uint8_t *dev = static_cast<const uint8_t *>(l.device);
-    if (l.host->state_bits == 8)
-      adamw_kernel<8><<<(uint32_t)(c1 - c0), 256, 0, stream>>>(dev, (int)t0, (int)t1, c0, l.s, g);
-    else
-      adamw_kernel<32><<<(uint32_t)(c1 - c0), 256, 0, stream>>>(dev, (int)t0, (int)t1, c0, l.s, g);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    // (a grid's threads are counted in 32 bits)
+    for (int64_t c = c0; c < c1; c += kMaxGrid) {
+      const uint32_t grid = (uint32_t)(c1 - c < kMaxGrid ? c1 - c : kMaxGrid);
+      if (l.host->state_bits == 8) adamw_kernel<8><<<grid, 256, 0, stream>>>(dev, (int)t0, (int)t1, c, l.s, g);
+      else adamw_kernel<32><<<grid, 256, 0, stream>>>(dev, (int)t0, (int)t1, c, l.s, g);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   return hipSuccess;
 }
 
 hipError_t launch_adamw_moments(const AdamMoments &l, hipStream_t stream) {
-  const int64_t wgs = (l.n + 2047) / 2048;
+  const int64_t need = (l.n + 2047) / 2048, most = 1 << 20;
+  const int64_t wgs = need < most ? need : most;
   if (l.out_f32)
     moments_kernel<true><<<(uint32_t)wgs, 256, 0, stream>>>(l);
   else
