@@ -10,8 +10,8 @@
 // Bound: HBM.  Per element the step reads and writes the weight and both moments and reads
 // the gradient once; no value is needed twice.
 //
-// Work division: a workgroup takes one chunk of kAdamChunk elements of one tensor, found by
-// bisection in the table's running chunk counts; the launch covers every chunk of up to
+// Work division: a workgroup takes one chunk of kAdamChunk elements of one tensor, found in
+// the table's running chunk counts; the launch covers every chunk of up to
 // kAdamGrads tensors, whose gradient pointers travel in the kernel's arguments.
 //
 // 8-bit moments: a lane holds 8 consecutive elements, half a wave one block of 256; the
@@ -135,10 +135,18 @@ __device__ __forceinline__ uint32_t lane_draw(const Philox4 &d, int j) {
   return (j & 1) ? w >> 16 : w & 0xFFFFu;
 }
 
-__device__ __forceinline__ float root_decode(uint32_t c) {
+// Values of the 256 codes, in LDS: a read there costs the vector units less than forming the
+// value (the 8-bit step is bound by their instructions).
+__device__ __forceinline__ float root_value(uint32_t c) {
   const uint32_t e = c >> 4, f = c & 15u;
   const float v = (float)(e ? (16u + f) << e : 2u * f);
   return c == 255u ? __uint_as_float(0x7FC00000u) : v;
+}
+
+// By 256 threads; a barrier follows.
+__device__ __forceinline__ void fill_roots(float *table) {
+  table[threadIdx.x] = root_value(threadIdx.x);
+  __syncthreads();
 }
 
 // Scale and its inverse for a block whose largest finite magnitude has these bits.
@@ -152,12 +160,14 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top, uint32_t exponen
 
 // Code of t = r / scale in [0, 2^19): below 32 the grid step is 2, so 32 is added and the
 // mantissa of the sum counts steps; above, exponent and the four leading mantissa bits are
-// the code.  The draw is added to the 19 bits that are dropped.
+// the code.  The draw (of 16 bits, plus 1/2) is added to the 19 bits that are dropped.  A root
+// above zero has code 1 at least.
 __device__ __forceinline__ uint32_t root_encode(float t, uint32_t draw) {
   const bool low = t < 32.0f;
   const uint32_t bits = __float_as_uint(low ? t + 32.0f : t);
-  const uint32_t c = ((bits - 0x42000000u + 8u * draw + 4u) >> 19) + (low ? 0u : 16u);
-  return t > 0.0f ? min(max(c, 1u), 254u) : 0u;
+  const uint32_t base = low ? 4u - 0x42000000u : 4u - 0x42000000u + (16u << 19);
+  const uint32_t c = (bits + (base + (draw << 3))) >> 19;
+  return min(max(c, min(__float_as_uint(t), 1u)), 254u);
 }
 
 // What a chunk's elements need of their tensor.
@@ -167,161 +177,162 @@ struct Chunk {
   uint32_t tensor;
   int64_t begin, end;
   float keep, gs;
+  const float *roots;   // fill_roots' table (8-bit moments)
 };
 
-// The elements begin .. end - 1.  WHOLE: they are a whole chunk; otherwise every access is
+// E elements per lane from i on.  WHOLE: the wave has all of them; otherwise every access is
 // bounded element by element.
 template <int BITS, bool PF, bool MASTER, bool GF, bool WHOLE>
-__device__ __forceinline__ void update(const Chunk &ch, const AdamScalars &s) {
+__device__ __forceinline__ void update(const Chunk &ch, const AdamScalars &s, int64_t i) {
   constexpr int E = BITS == 8 ? 8 : 4;
   const nvfp4_adamw_tensor &t = *ch.t;
   void *const param = t.param, *const exp_avg = t.exp_avg, *const exp_avg_sq = t.exp_avg_sq;
   float *const master = t.master, *const scale_m = t.exp_avg_scale, *const scale_r = t.exp_avg_sq_scale;
-  for (int64_t i0 = ch.begin + (threadIdx.x & ~63) * E; i0 < ch.end; i0 += 256 * E) {
-    const int64_t i = i0 + (threadIdx.x & 63) * E;
-    const int cnt = WHOLE ? E : (int)max((int64_t)0, min((int64_t)E, ch.end - i));
-    float g[E], w[E], m[E], v[E], r[E];
-    load_values<WHOLE, GF, E>(ch.g, i, cnt, g);
-    if constexpr (MASTER) load_values<WHOLE, true, E>(master, i, cnt, w);
-    else load_values<WHOLE, PF, E>(param, i, cnt, w);
-    if constexpr (BITS == 32) {
-      load_values<WHOLE, true, E>(exp_avg, i, cnt, m);
-      load_values<WHOLE, true, E>(exp_avg_sq, i, cnt, v);
+  const int cnt = WHOLE ? E : (int)max((int64_t)0, min((int64_t)E, ch.end - i));
+  float g[E], w[E], m[E], v[E], r[E];
+  load_values<WHOLE, GF, E>(ch.g, i, cnt, g);
+  if constexpr (MASTER) load_values<WHOLE, true, E>(master, i, cnt, w);
+  else load_values<WHOLE, PF, E>(param, i, cnt, w);
+  if constexpr (BITS == 32) {
+    load_values<WHOLE, true, E>(exp_avg, i, cnt, m);
+    load_values<WHOLE, true, E>(exp_avg_sq, i, cnt, v);
+  } else {
+    const uint8_t *pm = static_cast<const uint8_t *>(exp_avg) + i, *pv = static_cast<const uint8_t *>(exp_avg_sq) + i;
+    uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
+    float ms = 0.0f, vs = 0.0f;
+    if constexpr (WHOLE) {
+      const uint2 a = *reinterpret_cast<const uint2 *>(pm), b = *reinterpret_cast<const uint2 *>(pv);
+      mc[0] = a.x; mc[1] = a.y;
+      vc[0] = b.x; vc[1] = b.y;
     } else {
-      const uint8_t *pm = static_cast<const uint8_t *>(exp_avg) + i, *pv = static_cast<const uint8_t *>(exp_avg_sq) + i;
-      uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
-      float ms = 0.0f, vs = 0.0f;
-      if constexpr (WHOLE) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(pm), b = *reinterpret_cast<const uint2 *>(pv);
-        mc[0] = a.x; mc[1] = a.y;
-        vc[0] = b.x; vc[1] = b.y;
-      } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (j < cnt) {
-            mc[j >> 2] |= (uint32_t)pm[j] << (8 * (j & 3));
-            vc[j >> 2] |= (uint32_t)pv[j] << (8 * (j & 3));
-          }
-      }
-      if (WHOLE || cnt > 0) {
-        ms = scale_m[i / NVFP4_ADAMW_BLOCK];
-        vs = scale_r[i / NVFP4_ADAMW_BLOCK];
-      }
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        m[j] = e4m3_decode((mc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * ms;
-        const float q = root_decode((vc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * vs;
-        v[j] = q * q;
-      }
+      for (int j = 0; j < E; ++j)
+        if (j < cnt) {
+          mc[j >> 2] |= (uint32_t)pm[j] << (8 * (j & 3));
+          vc[j >> 2] |= (uint32_t)pv[j] << (8 * (j & 3));
+        }
+    }
+    if (WHOLE || cnt > 0) {
+      ms = scale_m[i / NVFP4_ADAMW_BLOCK];
+      vs = scale_r[i / NVFP4_ADAMW_BLOCK];
     }
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float gj = s.grad_scale ? g[j] * ch.gs : g[j];
-      m[j] = s.beta1 * m[j] + s.omb1 * gj;
-      v[j] = s.beta2 * v[j] + s.omb2 * (gj * gj);
-      r[j] = sqrtf(v[j]);
-      w[j] = w[j] * ch.keep - s.rate * (m[j] / (r[j] * s.root + s.eps));
+      m[j] = e4m3_decode((mc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * ms;
+      const float q = ch.roots[(vc[j >> 2] >> (8 * (j & 3))) & 0xFFu] * vs;
+      v[j] = q * q;
     }
-    if constexpr (MASTER) store_f32<WHOLE, E>(master, i, cnt, w);
-    if constexpr (PF) {
-      store_f32<WHOLE, E>(static_cast<float *>(param), i, cnt, w);
-    } else {
-      uint32_t b[E / 2];
-      if (s.stochastic_param) {
-        const Philox4 d = draws8(i >> 3, s, ch.tensor, 1u);
-        // (E = 4: the lanes of the upper half of eight take the last two words)
-        const uint32_t words[4] = {E == 4 && (i & 4) ? d.z : d.x, E == 4 && (i & 4) ? d.w : d.y, d.z, d.w};
+  }
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-          const float a = w[2 * j], c = w[2 * j + 1];
-          const uint32_t lo = __float_as_uint(a) + (words[j] & 0xFFFFu), hi = __float_as_uint(c) + (words[j] >> 16);
-          b[j] = (lo >> 16) | (hi & 0xFFFF0000u);
-          if (!finite_bits(a) || !finite_bits(c)) {   // inf and NaN take no draw
-            const uint32_t n = pack2(a, c);
-            if (!finite_bits(a)) b[j] = (b[j] & 0xFFFF0000u) | (n & 0xFFFFu);
-            if (!finite_bits(c)) b[j] = (b[j] & 0xFFFFu) | (n & 0xFFFF0000u);
-          }
+  for (int j = 0; j < E; ++j) {
+    const float gj = s.grad_scale ? g[j] * ch.gs : g[j];
+    m[j] = s.beta1 * m[j] + s.omb1 * gj;
+    v[j] = s.beta2 * v[j] + s.omb2 * (gj * gj);
+    r[j] = sqrtf(v[j]);
+    w[j] = w[j] * ch.keep - s.rate * (m[j] / (r[j] * s.root + s.eps));
+  }
+  if constexpr (MASTER) store_f32<WHOLE, E>(master, i, cnt, w);
+  if constexpr (PF) {
+    store_f32<WHOLE, E>(static_cast<float *>(param), i, cnt, w);
+  } else {
+    uint32_t b[E / 2];
+    if (s.stochastic_param) {
+      const Philox4 d = draws8(i >> 3, s, ch.tensor, 1u);
+      // (E = 4: the lanes of the upper half of eight take the last two words)
+      const uint32_t words[4] = {E == 4 && (i & 4) ? d.z : d.x, E == 4 && (i & 4) ? d.w : d.y, d.z, d.w};
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) {
+        const float a = w[2 * j], c = w[2 * j + 1];
+        const uint32_t lo = __float_as_uint(a) + (words[j] & 0xFFFFu), hi = __float_as_uint(c) + (words[j] >> 16);
+        b[j] = (lo >> 16) | (hi & 0xFFFF0000u);
+        if (!finite_bits(a) || !finite_bits(c)) {   // inf and NaN take no draw
+          const uint32_t n = pack2(a, c);
+          if (!finite_bits(a)) b[j] = (b[j] & 0xFFFF0000u) | (n & 0xFFFFu);
+          if (!finite_bits(c)) b[j] = (b[j] & 0xFFFFu) | (n & 0xFFFF0000u);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < E / 2; ++j) b[j] = pack2(w[2 * j], w[2 * j + 1]);
       }
-      store_u16<WHOLE, E>(static_cast<uint16_t *>(param), i, cnt, b);
-    }
-    if constexpr (BITS == 32) {
-      store_f32<WHOLE, E>(static_cast<float *>(exp_avg), i, cnt, m);
-      store_f32<WHOLE, E>(static_cast<float *>(exp_avg_sq), i, cnt, v);
     } else {
-      uint32_t topm = 0u, topr = 0u;
-      bool odd = false;   // a moment that is not finite
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) b[j] = pack2(w[2 * j], w[2 * j + 1]);
+    }
+    store_u16<WHOLE, E>(static_cast<uint16_t *>(param), i, cnt, b);
+  }
+  if constexpr (BITS == 32) {
+    store_f32<WHOLE, E>(static_cast<float *>(exp_avg), i, cnt, m);
+    store_f32<WHOLE, E>(static_cast<float *>(exp_avg_sq), i, cnt, v);
+  } else {
+    uint32_t topm = 0u, topr = 0u;
+    bool odd = false;   // a moment that is not finite
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if (!WHOLE && j >= cnt) continue;
+      const uint32_t am = __float_as_uint(m[j]) & 0x7FFFFFFFu, ar = __float_as_uint(r[j]) & 0x7FFFFFFFu;
+      odd |= max(am, ar) >= 0x7F800000u;
+      topm = max(topm, am);
+      topr = max(topr, ar);
+    }
+    if (__any(odd)) {   // (they do not enter the block's scale)
+      topm = topr = 0u;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         if (!WHOLE && j >= cnt) continue;
-        const uint32_t am = __float_as_uint(m[j]) & 0x7FFFFFFFu, ar = __float_as_uint(r[j]) & 0x7FFFFFFFu;
-        odd |= max(am, ar) >= 0x7F800000u;
-        topm = max(topm, am);
-        topr = max(topr, ar);
-      }
-      if (__any(odd)) {   // (they do not enter the block's scale)
-        topm = topr = 0u;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          if (!WHOLE && j >= cnt) continue;
-          if (finite_bits(m[j])) topm = max(topm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-          if (finite_bits(r[j])) topr = max(topr, __float_as_uint(r[j]));
-        }
-      }
-      const BlockScale bm = block_scale(half_max(topm), kExpM), br = block_scale(half_max(topr), kExpR);
-      const bool live = bm.scale > 0.0f;
-      const Philox4 d = draws8(i >> 3, s, ch.tensor, 0u);
-      uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        const float a = m[j] * bm.inv, b = m[j + 1] * bm.inv, c = m[j + 2] * bm.inv, e = m[j + 3] * bm.inv;
-        uint32_t q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-        q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, e, (int)q, true);
-        mc[j >> 2] = live ? q : 0u;
-#pragma unroll
-        for (int l = 0; l < 4; ++l) vc[j >> 2] |= root_encode(r[j + l] * br.inv, lane_draw(d, j + l)) << (8 * l);
-      }
-      if (__any(odd)) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const uint32_t byte = 0xFFu << (8 * (j & 3));
-          if (!finite_bits(m[j])) mc[j >> 2] = (mc[j >> 2] & ~byte) | (0x7Fu << (8 * (j & 3)));
-          if (!finite_bits(r[j])) vc[j >> 2] |= byte;
-        }
-      }
-      uint8_t *pm = static_cast<uint8_t *>(exp_avg) + i, *pv = static_cast<uint8_t *>(exp_avg_sq) + i;
-      if constexpr (WHOLE) {
-        *reinterpret_cast<uint2 *>(pm) = make_uint2(mc[0], mc[1]);
-        *reinterpret_cast<uint2 *>(pv) = make_uint2(vc[0], vc[1]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (j < cnt) {
-            pm[j] = (uint8_t)(mc[j >> 2] >> (8 * (j & 3)));
-            pv[j] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
-          }
-      }
-      if ((WHOLE || cnt > 0) && (threadIdx.x & 31) == 0) {
-        scale_m[i / NVFP4_ADAMW_BLOCK] = bm.scale;
-        scale_r[i / NVFP4_ADAMW_BLOCK] = br.scale;
+        if (finite_bits(m[j])) topm = max(topm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+        if (finite_bits(r[j])) topr = max(topr, __float_as_uint(r[j]));
       }
     }
+    const BlockScale bm = block_scale(half_max(topm), kExpM), br = block_scale(half_max(topr), kExpR);
+    const bool live = bm.scale > 0.0f;
+    const Philox4 d = draws8(i >> 3, s, ch.tensor, 0u);
+    uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float a = m[j] * bm.inv, b = m[j + 1] * bm.inv, c = m[j + 2] * bm.inv, e = m[j + 3] * bm.inv;
+      uint32_t q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+      q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, e, (int)q, true);
+      mc[j >> 2] = live ? q : 0u;
+#pragma unroll
+      for (int l = 0; l < 4; ++l) vc[j >> 2] |= root_encode(r[j + l] * br.inv, lane_draw(d, j + l)) << (8 * l);
+    }
+    if (__any(odd)) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const uint32_t byte = 0xFFu << (8 * (j & 3));
+        if (!finite_bits(m[j])) mc[j >> 2] = (mc[j >> 2] & ~byte) | (0x7Fu << (8 * (j & 3)));
+        if (!finite_bits(r[j])) vc[j >> 2] |= byte;
+      }
+    }
+    uint8_t *pm = static_cast<uint8_t *>(exp_avg) + i, *pv = static_cast<uint8_t *>(exp_avg_sq) + i;
+    if constexpr (WHOLE) {
+      *reinterpret_cast<uint2 *>(pm) = make_uint2(mc[0], mc[1]);
+      *reinterpret_cast<uint2 *>(pv) = make_uint2(vc[0], vc[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (j < cnt) {
+          pm[j] = (uint8_t)(mc[j >> 2] >> (8 * (j & 3)));
+          pv[j] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
+        }
+    }
+    if ((WHOLE || cnt > 0) && (threadIdx.x & 31) == 0) {
+      scale_m[i / NVFP4_ADAMW_BLOCK] = bm.scale;
+      scale_r[i / NVFP4_ADAMW_BLOCK] = br.scale;
+    }
+  }
+}
+
+template <int BITS, bool PF, bool MASTER, bool GF>
+__device__ __forceinline__ void update_chunk(const Chunk &c, const AdamScalars &s) {
+  constexpr int E = BITS == 8 ? 8 : 4;
+  for (int64_t i = c.begin + (threadIdx.x & ~63) * E; i < c.end; i += 256 * E) {
+    if (i + 64 * E <= c.end) update<BITS, PF, MASTER, GF, true>(c, s, i + (threadIdx.x & 63) * E);
+    else update<BITS, PF, MASTER, GF, false>(c, s, i + (threadIdx.x & 63) * E);
   }
 }
 
 template <int BITS, bool PF, bool MASTER>
 __device__ __forceinline__ void update_as(const Chunk &c, const AdamScalars &s) {
-  const bool whole = c.end - c.begin == kAdamChunk;
-  if (c.t->grad_dtype == NVFP4_DT_FP32) {
-    if (whole) update<BITS, PF, MASTER, true, true>(c, s);
-    else update<BITS, PF, MASTER, true, false>(c, s);
-  } else {
-    if (whole) update<BITS, PF, MASTER, false, true>(c, s);
-    else update<BITS, PF, MASTER, false, false>(c, s);
-  }
+  if (c.t->grad_dtype == NVFP4_DT_FP32) update_chunk<BITS, PF, MASTER, true>(c, s);
+  else update_chunk<BITS, PF, MASTER, false>(c, s);
 }
 
 template <int BITS>
@@ -329,12 +340,18 @@ __global__ __launch_bounds__(256) void adamw_kernel(const uint8_t *__restrict__ 
                                                     int64_t chunk0, AdamScalars s, GradPointers grads) {
   const AdamRow *rows = reinterpret_cast<const AdamRow *>(table + sizeof(AdamHeader));
   const int64_t chunk = chunk0 + blockIdx.x;
-  int lo = t0, hi = t1;   // the last tensor whose first chunk is at most `chunk`
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (rows[mid].first_chunk <= chunk) lo = mid; else hi = mid;
+  // the last tensor whose first chunk is at most `chunk`: the lanes of each wave look at 64
+  // tensors at a time, all of whose loads are in flight together
+  int lo = t0 - 1;
+#pragma unroll
+  for (int k = 0; k < (kAdamGrads + 63) / 64; ++k) {
+    const int t = t0 + 64 * k + ((int)threadIdx.x & 63);
+    if (t0 + 64 * k < t1) lo += __popcll(__ballot(t < t1 && rows[min(t, t1 - 1)].first_chunk <= chunk));
   }
   Chunk c;
+  __shared__ float roots[BITS == 8 ? 256 : 1];
+  if constexpr (BITS == 8) fill_roots(roots);
+  c.roots = roots;
   c.t = &rows[lo].t;
   c.g = grads.p[lo - t0];
   if (!c.g) return;
@@ -351,6 +368,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const uint8_t *__restrict__ 
 // One thread per 8 codes of each moment (the last thread bounds its accesses).
 template <bool F32>
 __global__ __launch_bounds__(256) void moments_kernel(AdamMoments l) {
+  __shared__ float roots[256];
+  fill_roots(roots);
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < l.n; i += (int64_t)gridDim.x * 2048) {
     const int cnt = (int)min((int64_t)8, l.n - i);
     const float ms = l.ms[i / NVFP4_ADAMW_BLOCK], vs = l.vs[i / NVFP4_ADAMW_BLOCK];
@@ -369,7 +388,7 @@ __global__ __launch_bounds__(256) void moments_kernel(AdamMoments l) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       m[j] = e4m3_decode((mc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * ms;
-      const float q = root_decode((vc[j >> 2] >> (8 * (j & 3))) & 0xFFu) * vs;
+      const float q = roots[(vc[j >> 2] >> (8 * (j & 3))) & 0xFFu] * vs;
       v[j] = q * q;
     }
     if constexpr (F32) {
