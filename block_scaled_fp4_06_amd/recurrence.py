@@ -104,20 +104,24 @@ def gated_scan_forward(g, u, floor=None, h0=None, reset=None, h_last=None, strea
 
 
 def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=None,
-                        stream=None) -> GatedScanGrads:
+                        stream=None, out=None) -> GatedScanGrads:
     """The gradients of gated_scan_forward from those of y (dy) and of h_last (dh_last, None:
-    zero); y as the forward call returned it."""
+    zero); y as the forward call returned it.  out: (dg, du) to write into, laid out as g and
+    u may be (the two halves of one projection's gradient, for example); neither may share
+    memory with an input."""
     import torch
     _check_inputs(g, u, floor, h0, reset)
     _sequence("dy", dy, g)
     _sequence("y", y, g)
     batch, time, chan = g.shape
     _state("dh_last", dh_last, (batch, chan), g)
+    if out is not None:
+        _sequence("out[0]", out[0], g)
+        _sequence("out[1]", out[1], g)
     dev = g.device
 
     def call(handle):
-        dg = new_like(g)
-        du = new_like(g)
+        dg, du = (new_like(g), new_like(g)) if out is None else out
         dh0 = torch.empty((batch, chan), dtype=torch.float32, device=dev)
         dfloor = None if floor is None else torch.empty_like(floor)
         need = N.nvfp4_gated_scan_workspace_bytes(batch, time, chan, 1)
@@ -127,7 +131,7 @@ def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=No
         check(N.nvfp4_gated_scan_backward(_args(g, u, floor, h0, reset, y, None), grads, ptr(ws),
                                           need, handle), "nvfp4_gated_scan_backward")
         return GatedScanGrads(dg, du, dh0, dfloor)
-    return run_on(stream, dev, (dy, g, u, y, floor, h0, reset, dh_last), call)
+    return run_on(stream, dev, (dy, g, u, y, floor, h0, reset, dh_last, *(out or ())), call)
 
 
 _AUTOGRAD = {}
