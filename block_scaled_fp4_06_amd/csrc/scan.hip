@@ -74,11 +74,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, Two{(__bf16)lo, (__bf16)hi});
 }
 
-// Elements from .. to - 1 of the V at p.
-template <bool F32>
+// Elements from .. to - 1 of the V at p; WHOLE: all of them.
+template <bool WHOLE, bool F32>
 __device__ __forceinline__ void store(char *p, int from, int to, const float (&v)[F32 ? 4 : 8]) {
   constexpr int V = F32 ? 4 : 8;
-  if (from <= 0 && to >= V) {
+  if (WHOLE || (from <= 0 && to >= V)) {
     Four f;
 #pragma unroll
     for (int l = 0; l < 4; ++l) f.w[l] = F32 ? __float_as_uint(v[l & 3]) : pack2(v[(2 * l) % V], v[(2 * l + 1) % V]);
@@ -148,11 +148,13 @@ __device__ __forceinline__ Pair then(const Pair &p, const Pair &q) {
 // (but the last) and channel, the state before every tile.
 struct Tiling {
   int64_t chunks;
+  int64_t chunk0, batch0;   // the launch's first tile and batch row (grids are bounded)
   Pair *pairs;        // [batch][chunk][channel]
   float *states;      // [batch][chunk][channel]
 };
 
-// Where a thread's V channels are: blockIdx.x counts strips of 8 V.  Its own are the
+// Where a thread's V channels are: blockIdx.x counts strips of 8 V (y tiles, z batch rows).
+// Its own are the
 // elements own .. cnt - 1 of the access at col.
 template <int V, bool PART>
 struct Place {
@@ -172,8 +174,8 @@ struct Place {
   }
 };
 
-// The channel that thread tid < 8 V of a tile looks after between the kernels (that of
-// element tid % V of lane tid / V), and whether it is that lane's own.
+// The channel of a strip's place tid that passes between the kernels (that of element
+// tid % V of lane tid / V), and whether it is that lane's own.
 template <int V, bool PART>
 __device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t chan, bool &own) {
   const int64_t c = first + tid;
@@ -185,6 +187,12 @@ __device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t ch
     own = tid % V >= moved;
     return c - moved;
   }
+}
+
+// Whether all of a tile's steps and of its strip's channels exist.
+template <int V>
+__device__ __forceinline__ bool whole_tile(const nvfp4_scan_args &a, int64_t j) {
+  return (j + 1) * kTile <= a.time && (int64_t)(blockIdx.x + 1) * (8 * V) <= a.chan;
 }
 
 // What the threads of a tile share.
@@ -246,10 +254,10 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, const float 
   return given ? given[batch * chan + c] : 0.0f;
 }
 
-// The first kernel: the pairs of all tiles but the last, which are whole.  A wave per tile,
-// kTile / 8 steps of V channels to a lane, four at a time with the next four's loads in
-// flight; the 8 groups of lanes are composed through LDS.  BACK: time runs backward, the
-// carries are c -> a (c + dy); `other` is dy, otherwise u.
+// The first kernel: the pairs of all tiles but the last, which are whole.  A wave per tile:
+// 8 groups of lanes share its steps, four steps at a time with the next four's loads in
+// flight, and are composed through LDS.  BACK: time runs backward, the carries are
+// c -> a (c + dy); `other` is dy, otherwise u.
 template <bool F32, bool BACK, bool RESET, bool FLOOR, bool PART>
 __global__ __launch_bounds__(64) void scan_pairs_kernel(nvfp4_scan_args a, const void *other,
                                                         int64_t other_batch, int64_t other_time,
@@ -260,69 +268,74 @@ __global__ __launch_bounds__(64) void scan_pairs_kernel(nvfp4_scan_args a, const
   const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
   float fl[V];
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
-  for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
-    for (int64_t j = blockIdx.y; j < tl.chunks - 1; j += gridDim.y) {
-      const int64_t i0 = j * kTile + group * kLong, t0 = BACK ? a.time - 1 - i0 : i0;
-      const int64_t sg = BACK ? -a.g_time : a.g_time, so = BACK ? -other_time : other_time;
-      const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
-      const char *po = at<F32>(other, batch * other_batch + t0 * other_time + pl.col);
-      Raw<F32> g[2][kAhead], o[2][kAhead];
-      auto fetch = [&](int q) {
+  const int64_t batch = tl.batch0 + blockIdx.z, j = tl.chunk0 + blockIdx.y;
+  const int64_t i0 = j * kTile + group * kLong, t0 = BACK ? a.time - 1 - i0 : i0;
+  const int64_t sg = BACK ? -a.g_time : a.g_time, so = BACK ? -other_time : other_time;
+  const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
+  const char *po = at<F32>(other, batch * other_batch + t0 * other_time + pl.col);
+  Raw<F32> g[2][kAhead], o[2][kAhead];
+  auto fetch = [&](int into) {
 #pragma unroll
-        for (int s = 0; s < kAhead; ++s) {
-          g[q & 1][s].template load<PART>(at<F32>(pg, (q * kAhead + s) * sg), pl.cnt);
-          o[q & 1][s].template load<PART>(at<F32>(po, (q * kAhead + s) * so), pl.cnt);
-        }
-      };
-      fetch(0);
-      Pair p[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
-#pragma unroll
-      for (int q = 0; q < kLong / kAhead; ++q) {
-        if (q + 1 < kLong / kAhead) fetch(q + 1);
-#pragma unroll
-        for (int s = 0; s < kAhead; ++s) {
-          const int64_t t = t0 + (BACK ? -1 : 1) * (q * kAhead + s);
-          const bool cut = RESET && (!PART || a.reset) && a.reset[batch * a.time + t];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float x, w;
-            decay<FLOOR>(g[q & 1][s].get(i), fl[i], x, w);
-            const float v = o[q & 1][s].get(i);
-            p[i] = Pair{x * p[i].a, BACK ? x * (p[i].b + v) : __builtin_fmaf(x, p[i].b, w * v)};
-            if (RESET && cut) p[i] = Pair{cut_mark(), BACK ? 0.0f : v};
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) groups[group][lane * V + i] = p[i];
-      __syncthreads();   // (one wave)
-      if (threadIdx.x < CH) {
-        bool own;
-        const int64_t c = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
-        Pair all = groups[0][threadIdx.x];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) all = then(all, groups[k][threadIdx.x]);
-        if (own) tl.pairs[(batch * tl.chunks + j) * a.chan + c] = all;
-      }
-      __syncthreads();
+    for (int s = 0; s < kAhead; ++s) {
+      g[into][s].template load<PART>(at<F32>(pg, s * sg), pl.cnt);
+      o[into][s].template load<PART>(at<F32>(po, s * so), pl.cnt);
     }
+    pg = at<F32>(pg, kAhead * sg);
+    po = at<F32>(po, kAhead * so);
+  };
+  fetch(0);
+  Pair p[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
+#pragma unroll
+  for (int q = 0; q < kLong / kAhead; ++q) {
+    if (q + 1 < kLong / kAhead) fetch((q + 1) & 1);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int64_t t = t0 + (BACK ? -1 : 1) * (q * kAhead + s);
+      const bool cut = RESET && (!PART || a.reset) && a.reset[batch * a.time + t];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float x, w;
+        decay<FLOOR>(g[q & 1][s].get(i), fl[i], x, w);
+        const float v = o[q & 1][s].get(i);
+        p[i] = Pair{x * p[i].a, BACK ? x * (p[i].b + v) : __builtin_fmaf(x, p[i].b, w * v)};
+      }
+      if (RESET && __any(cut)) {   // (one branch for the wave: resets are few)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (cut) p[i] = Pair{cut_mark(), BACK ? 0.0f : o[q & 1][s].get(i)};
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) groups[group][lane * V + i] = p[i];
+  __syncthreads();   // (one wave)
+  if (threadIdx.x < CH) {
+    bool own;
+    const int64_t c = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
+    Pair all = groups[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) all = then(all, groups[k][threadIdx.x]);
+    if (own) tl.pairs[(batch * tl.chunks + j) * a.chan + c] = all;
+  }
 }
 
-// The second kernel: a thread per batch row and channel walks over the tiles.
+// The second kernel: a thread per batch row and channel walks over the tiles, kWalk of whose
+// pairs it loads together.
+constexpr int kWalk = 16;
 __global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *given, int64_t chan,
                                                          int64_t threads) {
   for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
     const int64_t base = i / chan * t.chunks * chan + i % chan;
     float h = given ? given[i] : 0.0f;
-    for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += 32) {
-      Pair p[32];
+    for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += kWalk) {
+      Pair p[kWalk];
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
+      for (int k = 0; k < kWalk; ++k)
         if (j0 + k + 1 < t.chunks) p[k] = t.pairs[base + (j0 + k) * chan];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < kWalk; ++k) {
         if (j0 + k + 1 >= t.chunks) continue;
         h = apply(p[k], h);
         t.states[base + (j0 + k + 1) * chan] = h;
@@ -332,69 +345,84 @@ __global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *
 }
 
 // ---------------------------------------------------------------- forward
-// The third kernel.  Steps past the end (all in the last tile) read the last one again and
-// lead nowhere.
-template <bool F32, bool RESET, bool FLOOR, bool PART>
-__global__ __launch_bounds__(256) void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
+// One tile of the third kernel.  WHOLE: all its steps and channels exist.  Otherwise steps
+// past the end (all in the last tile) read the last one again and lead nowhere.
+template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
+__device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Tiling &tl, int64_t batch,
+                                             int64_t j, Shared<8 * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
-  __shared__ Shared<CH> sh;
   const Place<V, PART> pl(a.chan);
   const int group = threadIdx.x >> 3;
   float fl[V];
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
-  for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
-    for (int64_t j = blockIdx.y; j < tl.chunks; j += gridDim.y) {
-      const int64_t t0 = min(j * kTile + group * kSteps, a.time - 1);
-      const int more = (int)min((int64_t)kSteps, a.time - (j * kTile + group * kSteps));   // steps there are
-      const int last = max(0, more - 1);
-      const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
-      const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
-      Raw<F32> g[kSteps], u[kSteps];
+  const int64_t at0 = j * kTile + group * kSteps, t0 = WHOLE ? at0 : min(at0, a.time - 1);
+  const int more = WHOLE ? kSteps : (int)min((int64_t)kSteps, a.time - at0);   // steps there are
+  const int last = max(0, more - 1);
+  const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
+  const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
+  Raw<F32> g[kSteps], u[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        g[s].template load<PART>(at<F32>(pg, min(s, last) * a.g_time), pl.cnt);
-        u[s].template load<PART>(at<F32>(pu, min(s, last) * a.u_time), pl.cnt);
-      }
-      const float before = state_before_tile<V, PART>(tl, a.h0, batch, j, pl.first, a.chan);
-      float av[kSteps][V], bv[kSteps][V];
-      Pair p[V];
+  for (int s = 0; s < kSteps; ++s) {
+    g[s].template load<PART>(at<F32>(pg, (WHOLE ? s : min(s, last)) * a.g_time), pl.cnt);
+    u[s].template load<PART>(at<F32>(pu, (WHOLE ? s : min(s, last)) * a.u_time), pl.cnt);
+  }
+  const float before = state_before_tile<V, PART>(tl, a.h0, batch, j, pl.first, a.chan);
+  float av[kSteps][V], bv[kSteps][V];
+  Pair p[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
-      bool cut[kSteps];
+  for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
+  bool cut[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 + min(s, last)];
+  for (int s = 0; s < kSteps; ++s) {
+    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 + (WHOLE ? s : min(s, last))];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float w;
-          decay<FLOOR>(g[s].get(i), fl[i], av[s][i], w);
-          const float uv = u[s].get(i);
-          bv[s][i] = w * uv;
-          if (RESET && cut[s]) bv[s][i] = uv;
-          p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
-          if (RESET && cut[s]) p[i] = Pair{cut_mark(), bv[s][i]};
-        }
-      }
-      compose<V, CH>(sh, p);
-      float h[V];
-      states_of_groups<V, CH>(sh, before, h);
-      char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s >= more) break;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
-          if (RESET && cut[s]) h[i] = bv[s][i];
-        }
-        store<F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
-      }
-      if (a.h_last && j + 1 == tl.chunks && more > 0 && more <= kSteps && t0 + more == a.time)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
-      __syncthreads();   // before the next tile writes the shared words
+    for (int i = 0; i < V; ++i) {
+      float w;
+      decay<FLOOR>(g[s].get(i), fl[i], av[s][i], w);
+      const float uv = u[s].get(i);
+      bv[s][i] = w * uv;
+      p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
     }
+    if (RESET && __any(cut[s])) {   // (one branch for the wave: resets are few)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (cut[s]) {
+          bv[s][i] = u[s].get(i);
+          p[i] = Pair{cut_mark(), bv[s][i]};
+        }
+    }
+  }
+  compose<V, CH>(sh, p);
+  float h[V];
+  states_of_groups<V, CH>(sh, before, h);
+  char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (!WHOLE && s >= more) break;
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
+    if (RESET && __any(cut[s])) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (cut[s]) h[i] = bv[s][i];
+    }
+    store<WHOLE, F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
+  }
+  if (a.h_last && more > 0 && at0 + more == a.time)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
+}
+
+// The third kernel.  (One branch for a workgroup: no lane of most tiles has anything to
+// check.)
+template <bool F32, bool RESET, bool FLOOR, bool PART>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
+void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
+  __shared__ Shared<8 * Raw<F32>::V> sh;
+  const int64_t batch = tl.batch0 + blockIdx.z, j = tl.chunk0 + blockIdx.y;
+  if (!PART && whole_tile<Raw<F32>::V>(a, j)) forward_tile<F32, RESET, FLOOR, PART, true>(a, tl, batch, j, sh);
+  else forward_tile<F32, RESET, FLOOR, PART, false>(a, tl, batch, j, sh);
 }
 
 // A thread per V channels walks over the steps (the last thread of a row has the rest).
@@ -420,7 +448,7 @@ __global__ __launch_bounds__(64) void scan_forward_short_kernel(nvfp4_scan_args 
         const float rest = 1.0f - fl[k], x = __builtin_fmaf(rest, s, fl[k]);
         h[k] = cut ? u.get(k) : __builtin_fmaf(x, h[k], rest * sc * u.get(k));
       }
-      store<F32>(at<F32>(a.y, b * a.y_batch + t * a.y_time + col), 0, cnt, h);
+      store<false, F32>(at<F32>(a.y, b * a.y_batch + t * a.y_time + col), 0, cnt, h);
     }
     if (a.h_last)
 #pragma unroll
@@ -430,8 +458,9 @@ __global__ __launch_bounds__(64) void scan_forward_short_kernel(nvfp4_scan_args 
 }
 
 // ---------------------------------------------------------------- backward
-// One step: from dy and the carry c to dg, du and the next carry; adds to dfloor.
-template <bool F32, bool FLOOR>
+// One step: from dy and the carry c to dg, du and the next carry; adds to dfloor.  CUTS: it
+// may be a reset.
+template <bool F32, bool FLOOR, bool CUTS>
 __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> &u, const Raw<F32> &dy,
                                               const float (&before)[Raw<F32>::V], bool cut,
                                               const float (&fl)[Raw<F32>::V], float (&c)[Raw<F32>::V],
@@ -442,20 +471,25 @@ __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> 
     float s, sc;
     sigmoids(g.get(i), s, sc);
     const float rest = 1.0f - fl[i], grad = dy.get(i) + c[i], w = FLOOR ? rest * sc : sc;
-    const float da = grad * (before[i] - u.get(i));
-    du[i] = cut ? grad : w * grad;
-    dg[i] = cut ? 0.0f : da * (w * s);
-    if constexpr (FLOOR) dfl[i] = __builtin_fmaf(cut ? 0.0f : da, sc, dfl[i]);
-    c[i] = cut ? 0.0f : (FLOOR ? __builtin_fmaf(rest, s, fl[i]) : s) * grad;
+    float da = grad * (before[i] - u.get(i));
+    du[i] = w * grad;
+    dg[i] = da * (w * s);
+    c[i] = (FLOOR ? __builtin_fmaf(rest, s, fl[i]) : s) * grad;
+    if (CUTS && cut) {
+      du[i] = grad;
+      dg[i] = da = c[i] = 0.0f;
+    }
+    if constexpr (FLOOR) dfl[i] = __builtin_fmaf(da, sc, dfl[i]);
   }
 }
 
 // Time runs backward: a thread's step s is t = time - 1 - (j kTile + group kSteps + s).
-// Steps before the beginning (all in the last tile) read the first one again and lead nowhere.
-template <bool F32, bool RESET, bool FLOOR, bool PART>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
+// WHOLE: all the tile's steps and channels exist, and a step before each of them.  Otherwise
+// steps before the beginning (all in the last tile) read the first one again and lead nowhere.
+template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
+__device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling &tl, float *floors,
+                                              int64_t batch, int64_t j, Shared<8 * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
-  __shared__ Shared<CH> sh;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
   const Place<V, PART> pl(a.chan);
@@ -464,92 +498,103 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void s
 #pragma unroll
   for (int i = 0; i < V; ++i) fl[i] = 0.0f;
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
-  for (int64_t batch = blockIdx.z; batch < a.batch; batch += gridDim.z)
-    for (int64_t j = blockIdx.y; j < tl.chunks; j += gridDim.y) {
-      const int64_t steps = a.time - (j * kTile + group * kSteps);   // from the thread's first on
-      const int64_t t0 = max((int64_t)0, steps - 1);
-      const int more = (int)min((int64_t)kSteps, steps), last = max(0, more - 1);
-      const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
-      const char *pdy = at<F32>(d.dy, batch * d.dy_batch + t0 * d.dy_time + pl.col);
-      Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
+  const int64_t steps = a.time - (j * kTile + group * kSteps);   // from the thread's first on
+  const int64_t t0 = WHOLE ? steps - 1 : max((int64_t)0, steps - 1);
+  const int more = WHOLE ? kSteps : (int)min((int64_t)kSteps, steps), last = max(0, more - 1);
+  const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
+  const char *pdy = at<F32>(d.dy, batch * d.dy_batch + t0 * d.dy_time + pl.col);
+  Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        g[s].template load<PART>(at<F32>(pg, -min(s, last) * a.g_time), pl.cnt);
-        dy[s].template load<PART>(at<F32>(pdy, -min(s, last) * d.dy_time), pl.cnt);
-      }
-      const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
-      const char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
-      const int prior = (int)min((int64_t)kSteps, t0);   // (before the first step there is h0)
+  for (int s = 0; s < kSteps; ++s) {
+    g[s].template load<PART>(at<F32>(pg, -(WHOLE ? s : min(s, last)) * a.g_time), pl.cnt);
+    dy[s].template load<PART>(at<F32>(pdy, -(WHOLE ? s : min(s, last)) * d.dy_time), pl.cnt);
+  }
+  const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
+  const char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
+  const int prior = WHOLE ? kSteps : (int)min((int64_t)kSteps, t0);   // (before the first step there is h0)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        u[s].template load<PART>(at<F32>(pu, -min(s, last) * a.u_time), pl.cnt);
-        y[s].template load<PART>(at<F32>(py, -min(s + 1, prior) * a.y_time), pl.cnt);
-      }
-      const float before = state_before_tile<V, PART>(tl, d.dh_last, batch, j, pl.first, a.chan);
-      Pair p[V];
+  for (int s = 0; s < kSteps; ++s) {
+    u[s].template load<PART>(at<F32>(pu, -(WHOLE ? s : min(s, last)) * a.u_time), pl.cnt);
+    y[s].template load<PART>(at<F32>(py, -(WHOLE ? s + 1 : min(s + 1, prior)) * a.y_time), pl.cnt);
+  }
+  const float before = state_before_tile<V, PART>(tl, d.dh_last, batch, j, pl.first, a.chan);
+  Pair p[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
-      bool cut[kSteps];
+  for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
+  bool cut[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 - min(s, last)];
+  for (int s = 0; s < kSteps; ++s) {
+    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 - (WHOLE ? s : min(s, last))];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float x, w;
-          decay<FLOOR>(g[s].get(i), fl[i], x, w);
-          p[i] = Pair{x * p[i].a, x * (p[i].b + dy[s].get(i))};
-          if (RESET && cut[s]) p[i] = Pair{cut_mark(), 0.0f};
-        }
-      }
-      compose<V, CH>(sh, p);
-      float c[V], dfl[V];
-      states_of_groups<V, CH>(sh, before, c);
-      // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
-      char *pdg = at<F32>(d.dg, batch * d.dg_batch + t0 * d.dg_time + pl.col);
-      char *pdu = at<F32>(d.du, batch * d.du_batch + t0 * d.du_time + pl.col);
-#pragma unroll
-      for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s >= more) break;
-        float prior[V], dg[V], du[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) prior[i] = y[s].get(i);
-        if (t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior);
-        backward_step<F32, FLOOR>(g[s], u[s], dy[s], prior, RESET && cut[s], fl, c, dg, du, dfl);
-        store<F32>(at<F32>(pdg, -s * d.dg_time), pl.own, pl.cnt, dg);
-        store<F32>(at<F32>(pdu, -s * d.du_time), pl.own, pl.cnt, du);
-      }
-      if (d.dh0 && steps > 0 && steps <= kSteps)   // the thread with the first step
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i >= pl.own && i < pl.cnt) d.dh0[batch * a.chan + pl.col + i] = c[i];
-      if (d.dfloor) {   // the tile's sum over its steps, per channel
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < V; ++i) sh.group[group][lane * V + i].a = dfl[i];
-        __syncthreads();
-        const int ch = threadIdx.x % CH, seg = threadIdx.x / CH;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
-        sh.first[seg][ch] = sum;
-        __syncthreads();
-        if (threadIdx.x < CH) {
-          bool own;
-          const int64_t chan = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
-          sum = 0.0f;
-#pragma unroll
-          for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
-          if (own) floors[(batch * tl.chunks + j) * a.chan + chan] = sum;
-        }
-      }
-      __syncthreads();   // before the next tile writes the shared words
+    for (int i = 0; i < V; ++i) {
+      float x, w;
+      decay<FLOOR>(g[s].get(i), fl[i], x, w);
+      p[i] = Pair{x * p[i].a, x * (p[i].b + dy[s].get(i))};
     }
+    if (RESET && __any(cut[s])) {   // (one branch for the wave: resets are few)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (cut[s]) p[i] = Pair{cut_mark(), 0.0f};
+    }
+  }
+  compose<V, CH>(sh, p);
+  float c[V], dfl[V];
+  states_of_groups<V, CH>(sh, before, c);
+  // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
+  char *pdg = at<F32>(d.dg, batch * d.dg_batch + t0 * d.dg_time + pl.col);
+  char *pdu = at<F32>(d.du, batch * d.du_batch + t0 * d.du_time + pl.col);
+#pragma unroll
+  for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (!WHOLE && s >= more) break;
+    float prior_h[V], dg[V], du[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) prior_h[i] = y[s].get(i);
+    if (!WHOLE && t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior_h);
+    backward_step<F32, FLOOR, RESET>(g[s], u[s], dy[s], prior_h, RESET && cut[s], fl, c, dg, du, dfl);
+    store<WHOLE, F32>(at<F32>(pdg, -s * d.dg_time), pl.own, pl.cnt, dg);
+    store<WHOLE, F32>(at<F32>(pdu, -s * d.du_time), pl.own, pl.cnt, du);
+  }
+  if (!WHOLE && d.dh0 && steps > 0 && steps <= kSteps)   // the thread with the first step
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i >= pl.own && i < pl.cnt) d.dh0[batch * a.chan + pl.col + i] = c[i];
+  if (d.dfloor) {   // the tile's sum over its steps, per channel
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) sh.group[group][lane * V + i].a = dfl[i];
+    __syncthreads();
+    const int ch = threadIdx.x % CH, seg = threadIdx.x / CH;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Shared<CH>::kPer; ++i) sum += sh.group[seg * Shared<CH>::kPer + i][ch].a;
+    sh.first[seg][ch] = sum;
+    __syncthreads();
+    if (threadIdx.x < CH) {
+      bool own;
+      const int64_t chan = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
+      sum = 0.0f;
+#pragma unroll
+      for (int s = 0; s < Shared<CH>::kSegs; ++s) sum += sh.first[s][ch];
+      if (own) floors[(batch * tl.chunks + j) * a.chan + chan] = sum;
+    }
+  }
+}
+
+template <bool F32, bool RESET, bool FLOOR, bool PART>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
+void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
+  __shared__ Shared<8 * Raw<F32>::V> sh;
+  const int64_t batch = tl.batch0 + blockIdx.z, j = tl.chunk0 + blockIdx.y;
+  if (!PART && j + 1 < tl.chunks && whole_tile<Raw<F32>::V>(l.a, j))
+    backward_tile<F32, RESET, FLOOR, PART, true>(l, tl, floors, batch, j, sh);
+  else
+    backward_tile<F32, RESET, FLOOR, PART, false>(l, tl, floors, batch, j, sh);
 }
 
 template <bool F32, bool PART>
@@ -579,9 +624,9 @@ __global__ __launch_bounds__(64) void scan_backward_short_kernel(ScanLaunch l, i
       } else {
         load_f32<V, PART>(a.h0, b * a.chan + col, cnt, before);
       }
-      backward_step<F32, true>(g, u, dy, before, a.reset && a.reset[b * a.time + t], fl, c, dg, du, dfl);
-      store<F32>(at<F32>(d.dg, b * d.dg_batch + t * d.dg_time + col), 0, cnt, dg);
-      store<F32>(at<F32>(d.du, b * d.du_batch + t * d.du_time + col), 0, cnt, du);
+      backward_step<F32, true, true>(g, u, dy, before, a.reset && a.reset[b * a.time + t], fl, c, dg, du, dfl);
+      store<false, F32>(at<F32>(d.dg, b * d.dg_batch + t * d.dg_time + col), 0, cnt, dg);
+      store<false, F32>(at<F32>(d.du, b * d.du_batch + t * d.du_time + col), 0, cnt, du);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -632,14 +677,24 @@ Layout layout_of(int64_t batch, int64_t time, int64_t chan, bool backward) {
 
 Tiling tiling_of(const Layout &l, void *ws) {
   char *p = static_cast<char *>(ws);
-  return Tiling{l.chunks, reinterpret_cast<Pair *>(p), reinterpret_cast<float *>(p + l.states)};
+  return Tiling{l.chunks, 0, 0, reinterpret_cast<Pair *>(p), reinterpret_cast<float *>(p + l.states)};
 }
 
 uint32_t at_most(int64_t n, int64_t most) { return (uint32_t)(n < most ? n : most); }
 
-// (Channels beyond 2^31 are refused before; the other two step.)
-dim3 tile_grid(const nvfp4_scan_args &a, int64_t chunks, int ch) {
-  return dim3((uint32_t)((a.chan + ch - 1) / ch), at_most(chunks, 65535), at_most(a.batch, 65535));
+// Launches over all strips of `ch` channels, tiles and batch rows, the latter two in slices
+// that a grid can count.  launch(grid, tiling).
+template <class Launch>
+hipError_t over_tiles(const nvfp4_scan_args &a, Tiling t, int64_t chunks, int ch, Launch &&launch) {
+  constexpr int64_t most = 65535;
+  const uint32_t strips = (uint32_t)((a.chan + ch - 1) / ch);
+  for (t.batch0 = 0; t.batch0 < a.batch; t.batch0 += most)
+    for (t.chunk0 = 0; t.chunk0 < chunks; t.chunk0 += most) {
+      launch(dim3(strips, at_most(chunks - t.chunk0, most), at_most(a.batch - t.batch0, most)), t);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
 }
 
 hipError_t launch_states(const nvfp4_scan_args &a, const Tiling &t, const float *given, hipStream_t stream) {
@@ -648,34 +703,43 @@ hipError_t launch_states(const nvfp4_scan_args &a, const Tiling &t, const float 
   return hipGetLastError();
 }
 
+template <bool F32, bool BACK, bool RESET, bool FLOOR, bool PART>
+hipError_t launch_pairs(const nvfp4_scan_args &a, const void *other, int64_t other_batch,
+                        int64_t other_time, const Tiling &all, hipStream_t stream) {
+  return over_tiles(a, all, all.chunks - 1, 8 * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
+    scan_pairs_kernel<F32, BACK, RESET, FLOOR, PART><<<grid, 64, 0, stream>>>(a, other, other_batch,
+                                                                             other_time, t);
+  });
+}
+
 template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
-  const Tiling t = tiling_of(l, s.ws);
+  const Tiling all = tiling_of(l, s.ws);
   const int ch = 8 * Raw<F32>::V;
   hipError_t e;
   if (l.chunks > 1) {
-    scan_pairs_kernel<F32, false, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks - 1, ch), 64, 0, stream>>>(
-        s.a, s.a.u, s.a.u_batch, s.a.u_time, t);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_states(s.a, t, s.a.h0, stream)) != hipSuccess) return e;
+    e = launch_pairs<F32, false, RESET, FLOOR, PART>(s.a, s.a.u, s.a.u_batch, s.a.u_time, all, stream);
+    if (e != hipSuccess) return e;
+    if ((e = launch_states(s.a, all, s.a.h0, stream)) != hipSuccess) return e;
   }
-  scan_forward_kernel<F32, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s.a, t);
-  return hipGetLastError();
+  return over_tiles(s.a, all, l.chunks, ch, [&](dim3 grid, const Tiling &t) {
+    scan_forward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s.a, t);
+  });
 }
 
 template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
-  const Tiling t = tiling_of(l, s.ws);
+  const Tiling all = tiling_of(l, s.ws);
   const int ch = 8 * Raw<F32>::V;
   hipError_t e;
   if (l.chunks > 1) {
-    scan_pairs_kernel<F32, true, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks - 1, ch), 64, 0, stream>>>(
-        s.a, s.d.dy, s.d.dy_batch, s.d.dy_time, t);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_states(s.a, t, s.d.dh_last, stream)) != hipSuccess) return e;
+    e = launch_pairs<F32, true, RESET, FLOOR, PART>(s.a, s.d.dy, s.d.dy_batch, s.d.dy_time, all, stream);
+    if (e != hipSuccess) return e;
+    if ((e = launch_states(s.a, all, s.d.dh_last, stream)) != hipSuccess) return e;
   }
-  scan_backward_kernel<F32, RESET, FLOOR, PART><<<tile_grid(s.a, l.chunks, ch), 256, 0, stream>>>(s, t, floors);
-  return hipGetLastError();
+  return over_tiles(s.a, all, l.chunks, ch, [&](dim3 grid, const Tiling &t) {
+    scan_backward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s, t, floors);
+  });
 }
 
 template <bool F32>
