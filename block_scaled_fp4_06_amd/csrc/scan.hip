@@ -154,8 +154,7 @@ struct Tiling {
 };
 
 // Where a thread's V channels are: blockIdx.x counts strips of 8 V (y tiles, z batch rows).
-// Its own are the
-// elements own .. cnt - 1 of the access at col.
+// Its own are the elements own .. cnt - 1 of the access at col.
 template <int V, bool PART>
 struct Place {
   int64_t first, col;   // the strip's first channel; the thread's access
@@ -242,7 +241,8 @@ __device__ __forceinline__ void states_of_groups(Shared<CH> &sh, float before, f
     h[i] = apply(sh.group[group][lane * V + i], sh.first[group / Shared<CH>::kPer][lane * V + i]);
 }
 
-// The state before a tile: the second kernel's, or before the first tile the given one.
+// The state before a tile: the second kernel's, or where there is one tile the given one.
+// (Not the given one before a first tile of several: the last tile's h_last may be its place.)
 template <int V, bool PART>
 __device__ __forceinline__ float state_before_tile(const Tiling &t, const float *given, int64_t batch,
                                                    int64_t j, int64_t first, int64_t chan) {
@@ -250,7 +250,7 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, const float 
   bool own;
   const int64_t c = channel_of<V, PART>(threadIdx.x, first, chan, own);
   if (PART && !own) return 0.0f;
-  if (j > 0) return t.states[(batch * t.chunks + j) * chan + c];
+  if (t.chunks > 1) return t.states[(batch * t.chunks + j) * chan + c];
   return given ? given[batch * chan + c] : 0.0f;
 }
 
@@ -329,6 +329,7 @@ __global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *
   for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
     const int64_t base = i / chan * t.chunks * chan + i % chan;
     float h = given ? given[i] : 0.0f;
+    t.states[base] = h;
     for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += kWalk) {
       Pair p[kWalk];
 #pragma unroll

@@ -239,6 +239,18 @@ def test_state_kept_in_place_step_by_step():
     assert float((state - last).abs().max()) <= 64 * U * 8
 
 
+@pytest.mark.parametrize("b,t,c", [(2, 4500, 64), (64, 130, 200), (3, 100, 77), (5, 9, 13)])
+def test_long_sequences_keep_the_state_in_place(b, t, c):
+    say("scan %dx%dx%d with h_last in h0's place" % (b, t, c))
+    g, u, fl, h0, _ = case(b, t, c, BF16)
+    y, last = R.gated_scan_forward(g, u, fl, h0)
+    for _ in range(3):
+        state = h0.clone()
+        yi, s = R.gated_scan_forward(g, u, fl, state, h_last=state)
+        torch.cuda.synchronize()
+        assert s is state and torch.equal(yi, y) and torch.equal(state, last)
+
+
 def test_continuing_equals_the_whole():
     say("scan in two calls joined by the state")
     g, u, fl, h0, reset = case(2, 1100, 72, F32, docs=4)
