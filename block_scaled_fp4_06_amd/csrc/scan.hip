@@ -32,6 +32,8 @@ namespace {
 constexpr int kGroups = 32;          // time groups of a tile: 256 threads / 8 lanes of channels
 constexpr int kSteps = 4;            // steps of a thread
 constexpr int kTile = kGroups * kSteps;
+constexpr int kWindow = 8;           // tiles before its own that a tile looks at
+constexpr uint64_t kWaitTicks = 500000000ull;   // 5 s of the 100 MHz clock
 constexpr int kShort = 16;           // steps that one thread walks over by itself
 
 // ---------------------------------------------------------------- loads and stores
@@ -144,14 +146,35 @@ __device__ __forceinline__ Pair then(const Pair &p, const Pair &q) {
 }
 
 // ---------------------------------------------------------------- tiles
-// Tiles along time of every sequence, and what passes between the kernels: a pair per tile
-// (but the last) and channel, the state before every tile.
+// Tiles along time of every sequence, and what passes between them.  A strip (of one batch
+// row) counts its tiles as they are taken; a tile has a word per place: its pair, later
+// the state after it as the pair that leads there from anywhere.  Zero: neither yet.
 struct Tiling {
   int64_t chunks;
   int64_t chunk0, batch0;   // the launch's first tile and batch row (grids are bounded)
-  Pair *pairs;        // [batch][chunk][channel]
-  float *states;      // [batch][chunk][channel]
+  uint32_t *taken;          // [strip][kLine]
+  uint64_t *words;          // [strip][tile][place]
 };
+
+constexpr int kLine = 32;   // (128 bytes: strips do not share lines)
+
+// A word holds both numbers at once, so nothing has to be ordered around it.  The factor's
+// bits are inverted: no word is then zero, given that a NaN comes in one form.
+__device__ __forceinline__ uint64_t word_of(const Pair &p) {
+  const uint32_t a = p.a == p.a ? __float_as_uint(p.a) : 0x7FC00000u;
+  return ((uint64_t)__float_as_uint(p.b) << 32) | (uint32_t)~a;
+}
+__device__ __forceinline__ Pair pair_of(uint64_t w) {
+  return Pair{__uint_as_float(~(uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+
+// Stores and loads that go past the caches of one die.
+__device__ __forceinline__ uint64_t load_agent(const uint64_t *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void store_agent(uint64_t *p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 // Where a thread's V channels are: blockIdx.x counts strips of 8 V (y tiles, z batch rows).
 // Its own are the elements own .. cnt - 1 of the access at col.
@@ -173,8 +196,8 @@ struct Place {
   }
 };
 
-// The channel of a strip's place tid that passes between the kernels (that of element
-// tid % V of lane tid / V), and whether it is that lane's own.
+// The channel of a strip's place tid < 8 V (element tid % V of lane tid / V), whether there
+// is one, and whether it is that lane's own.
 template <int V, bool PART>
 __device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t chan, bool &own) {
   const int64_t c = first + tid;
@@ -201,6 +224,7 @@ struct Shared {
   Pair group[kGroups][CH];     // a group's pair, then that of its segment's groups before it
   Pair seg[kSegs][CH];
   float first[kSegs][CH];      // the state before a segment
+  uint32_t tile;
 };
 
 // The threads' pairs (one per channel) into segments' pairs; each group's place then holds
@@ -223,16 +247,69 @@ __device__ __forceinline__ void compose(Shared<CH> &sh, const Pair (&p)[V]) {
   __syncthreads();
 }
 
-// The state before each thread's steps from the one before the tile; `before` (per channel,
-// read by the first CH threads) and compose()'s result.
-template <int V, int CH>
-__device__ __forceinline__ void states_of_groups(Shared<CH> &sh, float before, float (&h)[V]) {
-  const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7;
-  if (tid < CH) {
+// The chain.  In wave 0, lane = place: from the tile's pair to the state before it, and what
+// other tiles need to know of both.  `given` is the state before the first tile.  States
+// follow from the one before by one pair, in order, however many of those a tile applies
+// itself: results do not depend on who was first.
+template <int CH>
+__device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t strip, int64_t j, const Pair &all,
+                                                   float given) {
+  const bool live = threadIdx.x < CH, more = j + 1 < t.chunks;
+  uint64_t *own = t.words + (strip * t.chunks + j) * CH + threadIdx.x % CH;
+  float before = given;
+  if (j > 0) {
+    if (live && more) store_agent(own, word_of(all));
+    const uint64_t start = wall_clock64();
+    const int reach = (int)min((int64_t)kWindow, j);
+    for (;;) {
+      uint64_t w[kWindow];
 #pragma unroll
-    for (int s = 0; s < Shared<CH>::kSegs; ++s) {
-      sh.first[s][tid] = before;
-      before = apply(sh.seg[s][tid], before);
+      for (int k = 0; k < kWindow; ++k) w[k] = load_agent(own - (int64_t)min(k + 1, reach) * CH);
+      // from the nearest state on (which needs none before it)
+      bool gap = true;
+#pragma unroll
+      for (int k = kWindow - 1; k >= 0; --k) {
+        const Pair p = pair_of(w[k]);
+        gap = w[k] == 0ull || (gap && !is_cut(p.a));
+        before = apply(p, before);
+      }
+      if (!__any(gap)) break;
+      if (wall_clock64() - start > kWaitTicks) {   // (never: see the order of the tiles)
+        before = __uint_as_float(0x7FC00000u);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+  }
+  if (live && more) store_agent(own, word_of(Pair{cut_mark(), apply(all, before)}));
+  return before;
+}
+
+// The state before each thread's steps from compose()'s result and the state before the
+// first tile (per channel).
+template <int V, bool PART>
+__device__ __forceinline__ void states_of_groups(Shared<8 * V> &sh, const Tiling &t, const float *given,
+                                                 int64_t batch, int64_t j, int64_t first, int64_t chan,
+                                                 float (&h)[V]) {
+  constexpr int CH = 8 * V, kSegs = Shared<CH>::kSegs;
+  const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7;
+  if (tid < 64) {
+    Pair all = sh.seg[0][tid % CH];
+#pragma unroll
+    for (int s = 1; s < kSegs; ++s) all = then(all, sh.seg[s][tid % CH]);
+    float before = 0.0f;
+    if (j == 0 && given && tid < CH) {
+      bool own;
+      const int64_t c = channel_of<V, PART>(tid, first, chan, own);
+      if (!PART || own) before = given[batch * chan + c];
+    }
+    if (t.chunks > 1) before = state_before_tile<CH>(t, batch * gridDim.x + blockIdx.x, j, all, before);
+    if (tid < CH) {
+#pragma unroll
+      for (int s = 0; s < kSegs; ++s) {
+        sh.first[s][tid] = before;
+        before = apply(sh.seg[s][tid], before);
+      }
     }
   }
   __syncthreads();
@@ -241,189 +318,147 @@ __device__ __forceinline__ void states_of_groups(Shared<CH> &sh, float before, f
     h[i] = apply(sh.group[group][lane * V + i], sh.first[group / Shared<CH>::kPer][lane * V + i]);
 }
 
-// The state before a tile: the second kernel's, or where there is one tile the given one.
-// (Not the given one before a first tile of several: the last tile's h_last may be its place.)
-template <int V, bool PART>
-__device__ __forceinline__ float state_before_tile(const Tiling &t, const float *given, int64_t batch,
-                                                   int64_t j, int64_t first, int64_t chan) {
-  if (threadIdx.x >= 8 * V) return 0.0f;
-  bool own;
-  const int64_t c = channel_of<V, PART>(threadIdx.x, first, chan, own);
-  if (PART && !own) return 0.0f;
-  if (t.chunks > 1) return t.states[(batch * t.chunks + j) * chan + c];
-  return given ? given[batch * chan + c] : 0.0f;
-}
+// The tile a workgroup takes: the next of its strip.  That is the one its place in the grid
+// suggests wherever workgroups begin in order, so the loads of that one can be on their way
+// while the count is asked for.
+template <int CH>
+struct Taken {
+  uint32_t number = 0;
+  __device__ __forceinline__ void ask(const Tiling &t, int64_t batch) {
+    if (t.chunks > 1 && threadIdx.x == 0)
+      number = __hip_atomic_fetch_add(t.taken + (batch * gridDim.x + blockIdx.x) * kLine, 1u,
+                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ int64_t tell(Shared<CH> &sh, const Tiling &t, int64_t guess) {
+    if (t.chunks == 1) return guess;
+    if (threadIdx.x == 0) sh.tile = number;
+    __syncthreads();
+    return (int64_t)__builtin_amdgcn_readfirstlane((int)sh.tile);
+  }
+};
 
-// The first kernel: the pairs of all tiles but the last, which are whole.  A wave per tile:
-// 8 groups of lanes share its steps, four steps at a time with the next four's loads in
-// flight, and are composed through LDS.  BACK: time runs backward, the carries are
-// c -> a (c + dy); `other` is dy, otherwise u.
-template <bool F32, bool BACK, bool RESET, bool FLOOR, bool PART>
-__global__ __launch_bounds__(64) void scan_pairs_kernel(nvfp4_scan_args a, const void *other,
-                                                        int64_t other_batch, int64_t other_time,
-                                                        Tiling tl) {
-  constexpr int V = Raw<F32>::V, CH = 8 * V, kLong = kTile / 8, kAhead = 4;
-  __shared__ Pair groups[8][CH];
-  const Place<V, PART> pl(a.chan);
-  const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
-  float fl[V];
-  if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
-  const int64_t batch = tl.batch0 + blockIdx.z, j = tl.chunk0 + blockIdx.y;
-  const int64_t i0 = j * kTile + group * kLong, t0 = BACK ? a.time - 1 - i0 : i0;
-  const int64_t sg = BACK ? -a.g_time : a.g_time, so = BACK ? -other_time : other_time;
-  const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
-  const char *po = at<F32>(other, batch * other_batch + t0 * other_time + pl.col);
-  Raw<F32> g[2][kAhead], o[2][kAhead];
-  auto fetch = [&](int into) {
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      g[into][s].template load<PART>(at<F32>(pg, s * sg), pl.cnt);
-      o[into][s].template load<PART>(at<F32>(po, s * so), pl.cnt);
-    }
-    pg = at<F32>(pg, kAhead * sg);
-    po = at<F32>(po, kAhead * so);
-  };
-  fetch(0);
-  Pair p[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
-#pragma unroll
-  for (int q = 0; q < kLong / kAhead; ++q) {
-    if (q + 1 < kLong / kAhead) fetch((q + 1) & 1);
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      const int64_t t = t0 + (BACK ? -1 : 1) * (q * kAhead + s);
-      const bool cut = RESET && (!PART || a.reset) && a.reset[batch * a.time + t];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float x, w;
-        decay<FLOOR>(g[q & 1][s].get(i), fl[i], x, w);
-        const float v = o[q & 1][s].get(i);
-        p[i] = Pair{x * p[i].a, BACK ? x * (p[i].b + v) : __builtin_fmaf(x, p[i].b, w * v)};
-      }
-      if (RESET && __any(cut)) {   // (one branch for the wave: resets are few)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (cut) p[i] = Pair{cut_mark(), BACK ? 0.0f : o[q & 1][s].get(i)};
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) groups[group][lane * V + i] = p[i];
-  __syncthreads();   // (one wave)
-  if (threadIdx.x < CH) {
-    bool own;
-    const int64_t c = channel_of<V, PART>(threadIdx.x, pl.first, a.chan, own);
-    Pair all = groups[0][threadIdx.x];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) all = then(all, groups[k][threadIdx.x]);
-    if (own) tl.pairs[(batch * tl.chunks + j) * a.chan + c] = all;
-  }
-}
-
-// The second kernel: a thread per batch row and channel walks over the tiles, kWalk of whose
-// pairs it loads together.
-constexpr int kWalk = 16;
-__global__ __launch_bounds__(64) void scan_states_kernel(Tiling t, const float *given, int64_t chan,
-                                                         int64_t threads) {
-  for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < threads; i += (int64_t)gridDim.x * 64) {
-    const int64_t base = i / chan * t.chunks * chan + i % chan;
-    float h = given ? given[i] : 0.0f;
-    t.states[base] = h;
-    for (int64_t j0 = 0; j0 + 1 < t.chunks; j0 += kWalk) {
-      Pair p[kWalk];
-#pragma unroll
-      for (int k = 0; k < kWalk; ++k)
-        if (j0 + k + 1 < t.chunks) p[k] = t.pairs[base + (j0 + k) * chan];
-#pragma unroll
-      for (int k = 0; k < kWalk; ++k) {
-        if (j0 + k + 1 >= t.chunks) continue;
-        h = apply(p[k], h);
-        t.states[base + (j0 + k + 1) * chan] = h;
-      }
-    }
-  }
+// Clears the words before a launch.
+__global__ __launch_bounds__(256) void scan_clear_kernel(uint4 *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ---------------------------------------------------------------- forward
-// One tile of the third kernel.  WHOLE: all its steps and channels exist.  Otherwise steps
-// past the end (all in the last tile) read the last one again and lead nowhere.
+// A thread's steps of tile j.  WHOLE: all the tile's steps and channels exist.  Otherwise
+// steps past the end (all in the last tile) read the last one again and lead nowhere.
+template <bool WHOLE>
+struct ForwardSteps {
+  int64_t at, t0;   // the first one, and the first one read
+  int more, last;   // how many there are; the last one read, from t0
+  __device__ __forceinline__ ForwardSteps(int64_t j, int64_t time) {
+    at = j * kTile + (threadIdx.x >> 3) * kSteps;
+    t0 = WHOLE ? at : min(at, time - 1);
+    more = WHOLE ? kSteps : (int)min((int64_t)kSteps, time - at);
+    last = max(0, more - 1);
+  }
+  __device__ __forceinline__ int step(int s) const { return WHOLE ? s : min(s, last); }
+};
+
+template <bool F32>
+struct ForwardLoads {
+  Raw<F32> g[kSteps], u[kSteps];
+  template <bool PART, bool WHOLE>
+  __device__ __forceinline__ void fetch(const nvfp4_scan_args &a, int64_t batch, int64_t j,
+                                        const Place<Raw<F32>::V, PART> &pl) {
+    const ForwardSteps<WHOLE> st(j, a.time);
+    const char *pg = at<F32>(a.g, batch * a.g_batch + st.t0 * a.g_time + pl.col);
+    const char *pu = at<F32>(a.u, batch * a.u_batch + st.t0 * a.u_time + pl.col);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      g[s].template load<PART>(at<F32>(pg, st.step(s) * a.g_time), pl.cnt);
+      u[s].template load<PART>(at<F32>(pu, st.step(s) * a.u_time), pl.cnt);
+    }
+  }
+};
+
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Tiling &tl, int64_t batch,
-                                             int64_t j, Shared<8 * Raw<F32>::V> &sh) {
+                                             int64_t j, const Place<Raw<F32>::V, PART> &pl,
+                                             ForwardLoads<F32> &in, Shared<8 * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
-  const Place<V, PART> pl(a.chan);
-  const int group = threadIdx.x >> 3;
+  Raw<F32>(&g)[kSteps] = in.g, (&u)[kSteps] = in.u;
+  const ForwardSteps<WHOLE> st(j, a.time);
   float fl[V];
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
-  const int64_t at0 = j * kTile + group * kSteps, t0 = WHOLE ? at0 : min(at0, a.time - 1);
-  const int more = WHOLE ? kSteps : (int)min((int64_t)kSteps, a.time - at0);   // steps there are
-  const int last = max(0, more - 1);
-  const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
-  const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
-  Raw<F32> g[kSteps], u[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    g[s].template load<PART>(at<F32>(pg, (WHOLE ? s : min(s, last)) * a.g_time), pl.cnt);
-    u[s].template load<PART>(at<F32>(pu, (WHOLE ? s : min(s, last)) * a.u_time), pl.cnt);
-  }
-  const float before = state_before_tile<V, PART>(tl, a.h0, batch, j, pl.first, a.chan);
-  float av[kSteps][V], bv[kSteps][V];
   Pair p[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
   bool cut[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 + (WHOLE ? s : min(s, last))];
+    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + st.t0 + st.step(s)];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float w;
-      decay<FLOOR>(g[s].get(i), fl[i], av[s][i], w);
-      const float uv = u[s].get(i);
-      bv[s][i] = w * uv;
-      p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
+      float x, w;
+      decay<FLOOR>(g[s].get(i), fl[i], x, w);
+      p[i] = Pair{x * p[i].a, __builtin_fmaf(x, p[i].b, w * u[s].get(i))};
     }
     if (RESET && __any(cut[s])) {   // (one branch for the wave: resets are few)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (cut[s]) {
-          bv[s][i] = u[s].get(i);
-          p[i] = Pair{cut_mark(), bv[s][i]};
-        }
+        if (cut[s]) p[i] = Pair{cut_mark(), u[s].get(i)};
     }
   }
   compose<V, CH>(sh, p);
   float h[V];
-  states_of_groups<V, CH>(sh, before, h);
-  char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
+  states_of_groups<V, PART>(sh, tl, a.h0, batch, j, pl.first, a.chan, h);
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
+  char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    if (!WHOLE && s >= more) break;
+    if (!WHOLE && s >= st.more) break;
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
+    for (int i = 0; i < V; ++i) {
+      float x, w;
+      decay<FLOOR>(g[s].get(i), fl[i], x, w);
+      h[i] = __builtin_fmaf(x, h[i], w * u[s].get(i));
+    }
     if (RESET && __any(cut[s])) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (cut[s]) h[i] = bv[s][i];
+        if (cut[s]) h[i] = u[s].get(i);
     }
     store<WHOLE, F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
   }
-  if (a.h_last && more > 0 && at0 + more == a.time)
+  if (a.h_last && st.more > 0 && st.at + st.more == a.time)
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
 }
 
-// The third kernel.  (One branch for a workgroup: no lane of most tiles has anything to
-// check.)
+// (One branch for a workgroup: no lane of most tiles has anything to check.)
 template <bool F32, bool RESET, bool FLOOR, bool PART>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
 void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
-  __shared__ Shared<8 * Raw<F32>::V> sh;
-  const int64_t batch = tl.batch0 + blockIdx.z, j = tl.chunk0 + blockIdx.y;
-  if (!PART && whole_tile<Raw<F32>::V>(a, j)) forward_tile<F32, RESET, FLOOR, PART, true>(a, tl, batch, j, sh);
-  else forward_tile<F32, RESET, FLOOR, PART, false>(a, tl, batch, j, sh);
+  constexpr int V = Raw<F32>::V;
+  __shared__ Shared<8 * V> sh;
+  const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
+  const Place<V, PART> pl(a.chan);
+  ForwardLoads<F32> in;
+  Taken<8 * V> taken;
+  taken.ask(tl, batch);
+  int64_t j = guess;
+  for (bool asked = false;;) {
+    in.template fetch<PART, false>(a, batch, j, pl);
+    if (asked) break;
+    const int64_t mine = taken.tell(sh, tl, guess);
+    if (mine == j) break;
+    asked = true;
+    j = mine;
+  }
+  if (!PART && whole_tile<V>(a, j)) {
+    forward_tile<F32, RESET, FLOOR, PART, true>(a, tl, batch, j, pl, in, sh);
+  } else {
+    forward_tile<F32, RESET, FLOOR, PART, false>(a, tl, batch, j, pl, in, sh);
+  }
 }
 
 // A thread per V channels walks over the steps (the last thread of a row has the rest).
@@ -487,45 +522,66 @@ __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> 
 // Time runs backward: a thread's step s is t = time - 1 - (j kTile + group kSteps + s).
 // WHOLE: all the tile's steps and channels exist, and a step before each of them.  Otherwise
 // steps before the beginning (all in the last tile) read the first one again and lead nowhere.
+template <bool WHOLE>
+struct BackwardSteps {
+  int64_t steps, t0;       // how many from the first one on to the beginning; the first one read
+  int more, last, prior;   // how many there are; the last one read, from t0; steps before t0
+  __device__ __forceinline__ BackwardSteps(int64_t j, int64_t time) {
+    steps = time - (j * kTile + (threadIdx.x >> 3) * kSteps);
+    t0 = WHOLE ? steps - 1 : max((int64_t)0, steps - 1);
+    more = WHOLE ? kSteps : (int)min((int64_t)kSteps, steps);
+    last = max(0, more - 1);
+    prior = WHOLE ? kSteps : (int)min((int64_t)kSteps, t0);
+  }
+  __device__ __forceinline__ int step(int s) const { return WHOLE ? s : min(s, last); }
+  __device__ __forceinline__ int before(int s) const { return WHOLE ? s + 1 : min(s + 1, prior); }
+};
+
+template <bool F32>
+struct BackwardLoads {
+  Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
+  template <bool PART, bool WHOLE>
+  __device__ __forceinline__ void fetch(const nvfp4_scan_args &a, const nvfp4_scan_grads &d, int64_t batch,
+                                        int64_t j, const Place<Raw<F32>::V, PART> &pl) {
+    const BackwardSteps<WHOLE> st(j, a.time);
+    const char *pg = at<F32>(a.g, batch * a.g_batch + st.t0 * a.g_time + pl.col);
+    const char *pdy = at<F32>(d.dy, batch * d.dy_batch + st.t0 * d.dy_time + pl.col);
+    const char *pu = at<F32>(a.u, batch * a.u_batch + st.t0 * a.u_time + pl.col);
+    const char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      g[s].template load<PART>(at<F32>(pg, -st.step(s) * a.g_time), pl.cnt);
+      dy[s].template load<PART>(at<F32>(pdy, -st.step(s) * d.dy_time), pl.cnt);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      u[s].template load<PART>(at<F32>(pu, -st.step(s) * a.u_time), pl.cnt);
+      y[s].template load<PART>(at<F32>(py, -st.before(s) * a.y_time), pl.cnt);
+    }
+  }
+};
+
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling &tl, float *floors,
-                                              int64_t batch, int64_t j, Shared<8 * Raw<F32>::V> &sh) {
+                                              int64_t batch, int64_t j, const Place<Raw<F32>::V, PART> &pl,
+                                              BackwardLoads<F32> &in, Shared<8 * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
-  const Place<V, PART> pl(a.chan);
   const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
+  Raw<F32>(&g)[kSteps] = in.g, (&dy)[kSteps] = in.dy, (&u)[kSteps] = in.u, (&y)[kSteps] = in.y;
+  const BackwardSteps<WHOLE> st(j, a.time);
   float fl[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) fl[i] = 0.0f;
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
-  const int64_t steps = a.time - (j * kTile + group * kSteps);   // from the thread's first on
-  const int64_t t0 = WHOLE ? steps - 1 : max((int64_t)0, steps - 1);
-  const int more = WHOLE ? kSteps : (int)min((int64_t)kSteps, steps), last = max(0, more - 1);
-  const char *pg = at<F32>(a.g, batch * a.g_batch + t0 * a.g_time + pl.col);
-  const char *pdy = at<F32>(d.dy, batch * d.dy_batch + t0 * d.dy_time + pl.col);
-  Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    g[s].template load<PART>(at<F32>(pg, -(WHOLE ? s : min(s, last)) * a.g_time), pl.cnt);
-    dy[s].template load<PART>(at<F32>(pdy, -(WHOLE ? s : min(s, last)) * d.dy_time), pl.cnt);
-  }
-  const char *pu = at<F32>(a.u, batch * a.u_batch + t0 * a.u_time + pl.col);
-  const char *py = at<F32>(a.y, batch * a.y_batch + t0 * a.y_time + pl.col);
-  const int prior = WHOLE ? kSteps : (int)min((int64_t)kSteps, t0);   // (before the first step there is h0)
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    u[s].template load<PART>(at<F32>(pu, -(WHOLE ? s : min(s, last)) * a.u_time), pl.cnt);
-    y[s].template load<PART>(at<F32>(py, -(WHOLE ? s + 1 : min(s + 1, prior)) * a.y_time), pl.cnt);
-  }
-  const float before = state_before_tile<V, PART>(tl, d.dh_last, batch, j, pl.first, a.chan);
   Pair p[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
   bool cut[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + t0 - (WHOLE ? s : min(s, last))];
+    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + st.t0 - st.step(s)];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float x, w;
@@ -540,28 +596,28 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
   }
   compose<V, CH>(sh, p);
   float c[V], dfl[V];
-  states_of_groups<V, CH>(sh, before, c);
+  states_of_groups<V, PART>(sh, tl, d.dh_last, batch, j, pl.first, a.chan, c);
   // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
 #pragma unroll
   for (int s = 0; s < kSteps; ++s)
 #pragma unroll
     for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
-  char *pdg = at<F32>(d.dg, batch * d.dg_batch + t0 * d.dg_time + pl.col);
-  char *pdu = at<F32>(d.du, batch * d.du_batch + t0 * d.du_time + pl.col);
+  char *pdg = at<F32>(d.dg, batch * d.dg_batch + st.t0 * d.dg_time + pl.col);
+  char *pdu = at<F32>(d.du, batch * d.du_batch + st.t0 * d.du_time + pl.col);
 #pragma unroll
   for (int i = 0; i < V; ++i) dfl[i] = 0.0f;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    if (!WHOLE && s >= more) break;
+    if (!WHOLE && s >= st.more) break;
     float prior_h[V], dg[V], du[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) prior_h[i] = y[s].get(i);
-    if (!WHOLE && t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior_h);
+    if (!WHOLE && st.t0 == s) load_f32<V, PART>(a.h0, batch * a.chan + pl.col, pl.cnt, prior_h);
     backward_step<F32, FLOOR, RESET>(g[s], u[s], dy[s], prior_h, RESET && cut[s], fl, c, dg, du, dfl);
     store<WHOLE, F32>(at<F32>(pdg, -s * d.dg_time), pl.own, pl.cnt, dg);
     store<WHOLE, F32>(at<F32>(pdu, -s * d.du_time), pl.own, pl.cnt, du);
   }
-  if (!WHOLE && d.dh0 && steps > 0 && steps <= kSteps)   // the thread with the first step
+  if (!WHOLE && d.dh0 && st.steps > 0 && st.steps <= kSteps)   // the thread with the first step
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i >= pl.own && i < pl.cnt) d.dh0[batch * a.chan + pl.col + i] = c[i];
@@ -590,12 +646,28 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
 template <bool F32, bool RESET, bool FLOOR, bool PART>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
-  __shared__ Shared<8 * Raw<F32>::V> sh;
-  const int64_t batch = tl.batch0 + blockIdx.z, j = tl.chunk0 + blockIdx.y;
-  if (!PART && j + 1 < tl.chunks && whole_tile<Raw<F32>::V>(l.a, j))
-    backward_tile<F32, RESET, FLOOR, PART, true>(l, tl, floors, batch, j, sh);
-  else
-    backward_tile<F32, RESET, FLOOR, PART, false>(l, tl, floors, batch, j, sh);
+  constexpr int V = Raw<F32>::V;
+  __shared__ Shared<8 * V> sh;
+  const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
+  const Place<V, PART> pl(l.a.chan);
+  BackwardLoads<F32> in;
+  Taken<8 * V> taken;
+  taken.ask(tl, batch);
+  auto whole = [&](int64_t j) { return !PART && j + 1 < tl.chunks && whole_tile<V>(l.a, j); };
+  int64_t j = guess;
+  for (bool asked = false;;) {
+    in.template fetch<PART, false>(l.a, l.d, batch, j, pl);
+    if (asked) break;
+    const int64_t mine = taken.tell(sh, tl, guess);
+    if (mine == j) break;
+    asked = true;
+    j = mine;
+  }
+  if (whole(j)) {
+    backward_tile<F32, RESET, FLOOR, PART, true>(l, tl, floors, batch, j, pl, in, sh);
+  } else {
+    backward_tile<F32, RESET, FLOOR, PART, false>(l, tl, floors, batch, j, pl, in, sh);
+  }
 }
 
 template <bool F32, bool PART>
@@ -659,26 +731,26 @@ __global__ __launch_bounds__(1024) void scan_floor_kernel(const float *sums, int
 // ---------------------------------------------------------------- launches
 constexpr int kCus = 256;
 
-// Workspace: the tiles' pairs and states (more than one tile), then their sums for dfloor
-// (backward).
+// Workspace (more than one tile): the strips' counts, the tiles' words; then the tiles' sums
+// for dfloor (backward).
 struct Layout {
   int64_t chunks;
-  size_t states, floors, bytes;   // offsets, and the whole
+  size_t words, floors, bytes;   // offsets, and the whole
 };
 
-Layout layout_of(int64_t batch, int64_t time, int64_t chan, bool backward) {
+Layout layout_of(int64_t batch, int64_t time, int64_t chan, int place, bool backward) {
   Layout l;
   l.chunks = time <= kShort ? 1 : (time + kTile - 1) / kTile;
-  const size_t n = (size_t)(batch * l.chunks * chan), tiled = l.chunks > 1 ? n : 0;
-  l.states = 8 * tiled;
-  l.floors = 12 * tiled;
-  l.bytes = l.floors + (backward ? 4 * n : 0);
+  const int64_t strips = l.chunks > 1 ? batch * ((chan + place - 1) / place) : 0;
+  l.words = 4 * (size_t)(strips * kLine);
+  l.floors = l.words + 8 * (size_t)(strips * l.chunks * place);
+  l.bytes = l.floors + (backward ? 4 * (size_t)(batch * l.chunks * chan) : 0);
   return l;
 }
 
 Tiling tiling_of(const Layout &l, void *ws) {
   char *p = static_cast<char *>(ws);
-  return Tiling{l.chunks, 0, 0, reinterpret_cast<Pair *>(p), reinterpret_cast<float *>(p + l.states)};
+  return Tiling{l.chunks, 0, 0, reinterpret_cast<uint32_t *>(p), reinterpret_cast<uint64_t *>(p + l.words)};
 }
 
 uint32_t at_most(int64_t n, int64_t most) { return (uint32_t)(n < most ? n : most); }
@@ -698,47 +770,27 @@ hipError_t over_tiles(const nvfp4_scan_args &a, Tiling t, int64_t chunks, int ch
   return hipSuccess;
 }
 
-hipError_t launch_states(const nvfp4_scan_args &a, const Tiling &t, const float *given, hipStream_t stream) {
-  const int64_t threads = a.batch * a.chan;
-  scan_states_kernel<<<at_most((threads + 63) / 64, 64 * kCus), 64, 0, stream>>>(t, given, a.chan, threads);
+hipError_t clear_words(const Layout &l, void *ws, hipStream_t stream) {
+  if (l.chunks == 1) return hipSuccess;
+  const int64_t n = (int64_t)(l.floors / 16);
+  scan_clear_kernel<<<at_most((n + 255) / 256, 4 * kCus), 256, 0, stream>>>(static_cast<uint4 *>(ws), n);
   return hipGetLastError();
-}
-
-template <bool F32, bool BACK, bool RESET, bool FLOOR, bool PART>
-hipError_t launch_pairs(const nvfp4_scan_args &a, const void *other, int64_t other_batch,
-                        int64_t other_time, const Tiling &all, hipStream_t stream) {
-  return over_tiles(a, all, all.chunks - 1, 8 * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
-    scan_pairs_kernel<F32, BACK, RESET, FLOOR, PART><<<grid, 64, 0, stream>>>(a, other, other_batch,
-                                                                             other_time, t);
-  });
 }
 
 template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
-  const Tiling all = tiling_of(l, s.ws);
-  const int ch = 8 * Raw<F32>::V;
-  hipError_t e;
-  if (l.chunks > 1) {
-    e = launch_pairs<F32, false, RESET, FLOOR, PART>(s.a, s.a.u, s.a.u_batch, s.a.u_time, all, stream);
-    if (e != hipSuccess) return e;
-    if ((e = launch_states(s.a, all, s.a.h0, stream)) != hipSuccess) return e;
-  }
-  return over_tiles(s.a, all, l.chunks, ch, [&](dim3 grid, const Tiling &t) {
+  const hipError_t e = clear_words(l, s.ws, stream);
+  if (e != hipSuccess) return e;
+  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, 8 * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
     scan_forward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s.a, t);
   });
 }
 
 template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
-  const Tiling all = tiling_of(l, s.ws);
-  const int ch = 8 * Raw<F32>::V;
-  hipError_t e;
-  if (l.chunks > 1) {
-    e = launch_pairs<F32, true, RESET, FLOOR, PART>(s.a, s.d.dy, s.d.dy_batch, s.d.dy_time, all, stream);
-    if (e != hipSuccess) return e;
-    if ((e = launch_states(s.a, all, s.d.dh_last, stream)) != hipSuccess) return e;
-  }
-  return over_tiles(s.a, all, l.chunks, ch, [&](dim3 grid, const Tiling &t) {
+  const hipError_t e = clear_words(l, s.ws, stream);
+  if (e != hipSuccess) return e;
+  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, 8 * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
     scan_backward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s, t, floors);
   });
 }
@@ -755,7 +807,7 @@ hipError_t run_forward(const ScanLaunch &s, hipStream_t stream) {
     else scan_forward_short_kernel<F32, false><<<grid, 64, 0, stream>>>(a, threads);
     return hipGetLastError();
   }
-  const Layout l = layout_of(a.batch, a.time, a.chan, false);
+  const Layout l = layout_of(a.batch, a.time, a.chan, 8 * V, false);
   if (few) return forward_tiles<F32, true, true, true>(s, l, stream);
   if (a.reset)
     return a.floor ? forward_tiles<F32, true, true, false>(s, l, stream)
@@ -769,7 +821,7 @@ hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
   constexpr int V = Raw<F32>::V;
   const nvfp4_scan_args &a = s.a;
   const bool few = a.chan < V;
-  const Layout l = layout_of(a.batch, a.time, a.chan, true);
+  const Layout l = layout_of(a.batch, a.time, a.chan, 8 * V, true);
   float *floors = reinterpret_cast<float *>(static_cast<char *>(s.ws) + l.floors);
   hipError_t e = hipSuccess;
   if (a.batch > 0) {
@@ -800,7 +852,9 @@ hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t batch, int64_t time, int64_t chan, bool backward) {
-  return layout_of(batch, time, chan, backward).bytes;
+  const size_t a = layout_of(batch, time, chan, 8 * Raw<false>::V, backward).bytes;
+  const size_t b = layout_of(batch, time, chan, 8 * Raw<true>::V, backward).bytes;
+  return a > b ? a : b;   // (of either type)
 }
 
 hipError_t launch_scan_forward(const ScanLaunch &s, hipStream_t stream) {
