@@ -13,16 +13,26 @@
 //  * A tile is 128 bytes of channels (8 lanes of 16 bytes) by kTile time steps: each of 256
 //    threads holds kSteps consecutive steps of its channels in registers.  A run of steps
 //    acts on the state as h -> A h + B; the threads' (A, B) are composed through LDS.
-//  * A sequence longer than a tile takes three kernels: the first forms every tile's (A, B)
-//    from g and u (backward: g and dy), the second walks over each channel's tiles and
-//    leaves the state before each, the third does the tiles.  What the first read is largely
-//    still in the 256 MB cache beside the memory when the third reads it again.  No
-//    workgroup waits for another, and every sum has one order.
+//  * The tiles of a sequence run in one kernel, so everything is read once.  A workgroup
+//    takes the next tile of its strip (a count in memory), so that it only ever waits for
+//    tiles that workgroups already run; it tells the others the tile's (A, B) if it has to
+//    wait, and the state behind the tile as soon as it knows it, each in one 64-bit word.
+//    The state before a tile is the nearest known one with the (A, B) of the tiles since
+//    applied to it in order: the same operations whoever was first, so results are the same
+//    every time.  (Three kernels, (A, B) of all tiles, then states, then tiles, read part of
+//    the inputs twice: 108 us forward, 152 us backward at the sizes below.)
 //  * A reset is a cut, not a product with zero: (cut, B) composed with anything before it is
 //    (cut, B), so inf and NaN end there.  A cut is held as A = -0.0, which no product of the
 //    other factors (in [0, 1], or NaN) gives.
 //
 // Few steps (up to kShort) need no tiles: a thread walks over them.
+//
+// Measured in bf16: forward with resets 8192 x 5120 in 77 us, 3.3 TB/s; backward with a
+// floor, 4 x 2048 x 5120, in 128 us, 3.9 TB/s (a copy reaches 5.1).  Without the exchange
+// between tiles they would take 70 and 125: the rest is one tile's way through load, LDS and
+// store, with 4 (backward 3) workgroups to a CU.  Longer runs per thread do not fit in
+// registers; tiles of 64 steps took 107 and 157 us, 4 workgroups backward 148.  One step
+// of 64 x 5120 takes 4.8 us.
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 
@@ -32,8 +42,9 @@ namespace {
 constexpr int kGroups = 32;          // time groups of a tile: 256 threads / 8 lanes of channels
 constexpr int kSteps = 4;            // steps of a thread
 constexpr int kTile = kGroups * kSteps;
-constexpr int kWindow = 8;           // tiles before its own that a tile looks at
-constexpr uint64_t kWaitTicks = 500000000ull;   // 5 s of the 100 MHz clock
+constexpr int kWindow = 4;           // tiles before its own that a tile looks at (1 to 8: alike here;
+                                     // few and long sequences gain from more than one)
+constexpr int kLooks = 1 << 22;      // how often a tile looks before it gives up: seconds
 constexpr int kShort = 16;           // steps that one thread walks over by itself
 
 // ---------------------------------------------------------------- loads and stores
@@ -258,10 +269,9 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
   uint64_t *own = t.words + (strip * t.chunks + j) * CH + threadIdx.x % CH;
   float before = given;
   if (j > 0) {
-    if (live && more) store_agent(own, word_of(all));
-    const uint64_t start = wall_clock64();
+    bool told = !more;   // (a pair is only for those who wait with this tile)
     const int reach = (int)min((int64_t)kWindow, j);
-    for (;;) {
+    for (int looks = 0;; ++looks) {
       uint64_t w[kWindow];
 #pragma unroll
       for (int k = 0; k < kWindow; ++k) w[k] = load_agent(own - (int64_t)min(k + 1, reach) * CH);
@@ -274,7 +284,9 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
         before = apply(p, before);
       }
       if (!__any(gap)) break;
-      if (wall_clock64() - start > kWaitTicks) {   // (never: see the order of the tiles)
+      if (!told && live) store_agent(own, word_of(all));
+      told = true;
+      if (looks == kLooks) {   // (never: see the order of the tiles)
         before = __uint_as_float(0x7FC00000u);
         break;
       }
@@ -302,6 +314,7 @@ __device__ __forceinline__ void states_of_groups(Shared<8 * V> &sh, const Tiling
       bool own;
       const int64_t c = channel_of<V, PART>(tid, first, chan, own);
       if (!PART || own) before = given[batch * chan + c];
+      asm volatile("" : "+v"(before));   // (waits here, not behind the chain's stores)
     }
     if (t.chunks > 1) before = state_before_tile<CH>(t, batch * gridDim.x + blockIdx.x, j, all, before);
     if (tid < CH) {
@@ -337,10 +350,10 @@ struct Taken {
   }
 };
 
-// Clears the words before a launch.
-__global__ __launch_bounds__(256) void scan_clear_kernel(uint4 *p, int64_t n) {
+// Clears counts and words before a launch, by the same way as they are used.
+__global__ __launch_bounds__(256) void scan_clear_kernel(uint64_t *p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
-    p[i] = make_uint4(0u, 0u, 0u, 0u);
+    store_agent(p + i, 0ull);
 }
 
 // ---------------------------------------------------------------- forward
@@ -359,9 +372,10 @@ struct ForwardSteps {
   __device__ __forceinline__ int step(int s) const { return WHOLE ? s : min(s, last); }
 };
 
-template <bool F32>
+template <bool F32, bool RESET>
 struct ForwardLoads {
   Raw<F32> g[kSteps], u[kSteps];
+  uint8_t reset[kSteps];
   template <bool PART, bool WHOLE>
   __device__ __forceinline__ void fetch(const nvfp4_scan_args &a, int64_t batch, int64_t j,
                                         const Place<Raw<F32>::V, PART> &pl) {
@@ -373,58 +387,58 @@ struct ForwardLoads {
       g[s].template load<PART>(at<F32>(pg, st.step(s) * a.g_time), pl.cnt);
       u[s].template load<PART>(at<F32>(pu, st.step(s) * a.u_time), pl.cnt);
     }
+    if (RESET && (!PART || a.reset))
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) reset[s] = a.reset[batch * a.time + st.t0 + st.step(s)];
   }
 };
 
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Tiling &tl, int64_t batch,
                                              int64_t j, const Place<Raw<F32>::V, PART> &pl,
-                                             ForwardLoads<F32> &in, Shared<8 * Raw<F32>::V> &sh) {
+                                             ForwardLoads<F32, RESET> &in, Shared<8 * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   Raw<F32>(&g)[kSteps] = in.g, (&u)[kSteps] = in.u;
   const ForwardSteps<WHOLE> st(j, a.time);
   float fl[V];
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
+  float av[kSteps][V], bv[kSteps][V];
   Pair p[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) p[i] = Pair{1.0f, 0.0f};
   bool cut[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + st.t0 + st.step(s)];
+    cut[s] = RESET && (!PART || a.reset) && in.reset[s];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float x, w;
-      decay<FLOOR>(g[s].get(i), fl[i], x, w);
-      p[i] = Pair{x * p[i].a, __builtin_fmaf(x, p[i].b, w * u[s].get(i))};
+      float w;
+      decay<FLOOR>(g[s].get(i), fl[i], av[s][i], w);
+      bv[s][i] = w * u[s].get(i);
+      p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
     }
     if (RESET && __any(cut[s])) {   // (one branch for the wave: resets are few)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (cut[s]) p[i] = Pair{cut_mark(), u[s].get(i)};
+        if (cut[s]) {
+          bv[s][i] = u[s].get(i);
+          p[i] = Pair{cut_mark(), bv[s][i]};
+        }
     }
   }
   compose<V, CH>(sh, p);
   float h[V];
   states_of_groups<V, PART>(sh, tl, a.h0, batch, j, pl.first, a.chan, h);
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
   char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     if (!WHOLE && s >= st.more) break;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float x, w;
-      decay<FLOOR>(g[s].get(i), fl[i], x, w);
-      h[i] = __builtin_fmaf(x, h[i], w * u[s].get(i));
-    }
+    for (int i = 0; i < V; ++i) h[i] = __builtin_fmaf(av[s][i], h[i], bv[s][i]);
     if (RESET && __any(cut[s])) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (cut[s]) h[i] = u[s].get(i);
+        if (cut[s]) h[i] = bv[s][i];
     }
     store<WHOLE, F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
   }
@@ -442,7 +456,7 @@ void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
   __shared__ Shared<8 * V> sh;
   const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
   const Place<V, PART> pl(a.chan);
-  ForwardLoads<F32> in;
+  ForwardLoads<F32, RESET> in;
   Taken<8 * V> taken;
   taken.ask(tl, batch);
   int64_t j = guess;
@@ -537,22 +551,33 @@ struct BackwardSteps {
   __device__ __forceinline__ int before(int s) const { return WHOLE ? s + 1 : min(s + 1, prior); }
 };
 
-template <bool F32>
+template <bool F32, bool RESET>
 struct BackwardLoads {
   Raw<F32> g[kSteps], dy[kSteps], u[kSteps], y[kSteps];
+  uint8_t reset[kSteps];
   template <bool PART, bool WHOLE>
   __device__ __forceinline__ void fetch(const nvfp4_scan_args &a, const nvfp4_scan_grads &d, int64_t batch,
                                         int64_t j, const Place<Raw<F32>::V, PART> &pl) {
     const BackwardSteps<WHOLE> st(j, a.time);
     const char *pg = at<F32>(a.g, batch * a.g_batch + st.t0 * a.g_time + pl.col);
     const char *pdy = at<F32>(d.dy, batch * d.dy_batch + st.t0 * d.dy_time + pl.col);
-    const char *pu = at<F32>(a.u, batch * a.u_batch + st.t0 * a.u_time + pl.col);
-    const char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       g[s].template load<PART>(at<F32>(pg, -st.step(s) * a.g_time), pl.cnt);
       dy[s].template load<PART>(at<F32>(pdy, -st.step(s) * d.dy_time), pl.cnt);
     }
+    if (RESET && (!PART || a.reset))
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) reset[s] = a.reset[batch * a.time + st.t0 - st.step(s)];
+  }
+  // What the second half needs, on its way while the first half's results are composed.
+  template <bool PART, bool WHOLE>
+  __device__ __forceinline__ void fetch_more(const nvfp4_scan_args &a, int64_t batch,
+                                             const BackwardSteps<WHOLE> &st,
+                                             const Place<Raw<F32>::V, PART> &pl) {
+    const char *pu = at<F32>(a.u, batch * a.u_batch + st.t0 * a.u_time + pl.col);
+    const char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       u[s].template load<PART>(at<F32>(pu, -st.step(s) * a.u_time), pl.cnt);
@@ -564,7 +589,7 @@ struct BackwardLoads {
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling &tl, float *floors,
                                               int64_t batch, int64_t j, const Place<Raw<F32>::V, PART> &pl,
-                                              BackwardLoads<F32> &in, Shared<8 * Raw<F32>::V> &sh) {
+                                              BackwardLoads<F32, RESET> &in, Shared<8 * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = 8 * V;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
@@ -581,7 +606,7 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
   bool cut[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    cut[s] = RESET && (!PART || a.reset) && a.reset[batch * a.time + st.t0 - st.step(s)];
+    cut[s] = RESET && (!PART || a.reset) && in.reset[s];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float x, w;
@@ -594,6 +619,11 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
         if (cut[s]) p[i] = Pair{cut_mark(), 0.0f};
     }
   }
+  if constexpr (FLOOR) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm volatile("" : "+v"(fl[i]));
+  }
+  in.template fetch_more<PART, WHOLE>(a, batch, st, pl);
   compose<V, CH>(sh, p);
   float c[V], dfl[V];
   states_of_groups<V, PART>(sh, tl, d.dh_last, batch, j, pl.first, a.chan, c);
@@ -601,7 +631,7 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
 #pragma unroll
   for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]));
+    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]), "+v"(dy[s].w[w]));
   char *pdg = at<F32>(d.dg, batch * d.dg_batch + st.t0 * d.dg_time + pl.col);
   char *pdu = at<F32>(d.du, batch * d.du_batch + st.t0 * d.du_time + pl.col);
 #pragma unroll
@@ -650,7 +680,7 @@ void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
   __shared__ Shared<8 * V> sh;
   const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
   const Place<V, PART> pl(l.a.chan);
-  BackwardLoads<F32> in;
+  BackwardLoads<F32, RESET> in;
   Taken<8 * V> taken;
   taken.ask(tl, batch);
   auto whole = [&](int64_t j) { return !PART && j + 1 < tl.chunks && whole_tile<V>(l.a, j); };
@@ -772,8 +802,8 @@ hipError_t over_tiles(const nvfp4_scan_args &a, Tiling t, int64_t chunks, int ch
 
 hipError_t clear_words(const Layout &l, void *ws, hipStream_t stream) {
   if (l.chunks == 1) return hipSuccess;
-  const int64_t n = (int64_t)(l.floors / 16);
-  scan_clear_kernel<<<at_most((n + 255) / 256, 4 * kCus), 256, 0, stream>>>(static_cast<uint4 *>(ws), n);
+  const int64_t n = (int64_t)(l.floors / 8);
+  scan_clear_kernel<<<at_most((n + 255) / 256, 8 * kCus), 256, 0, stream>>>(static_cast<uint64_t *>(ws), n);
   return hipGetLastError();
 }
 
