@@ -291,6 +291,26 @@ def test_repeats_are_identical():
             assert torch.equal(getattr(d[0], name), getattr(d[k], name)), name
 
 
+@pytest.mark.parametrize("b,t,c", [(24, 2500, 640), (3, 9000, 72)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_a_row_does_not_depend_on_the_others(b, t, c, dtype):
+    """More tiles than run at once, each waiting for the state before it."""
+    say("scan rows alone %dx%dx%d %s" % (b, t, c, dtype))
+    g, u, fl, h0, reset = case(b, t, c, dtype, seed=c)
+    dy, dh = rnd((b, t, c), dtype, 8), rnd((b, c), F32, 9)
+    y, last = R.gated_scan_forward(g, u, fl, h0, reset)
+    d = R.gated_scan_backward(dy, g, u, y, fl, h0, reset, dh)
+    for k in (0, b // 2, b - 1):
+        row = slice(k, k + 1)
+        r = None if reset is None else reset[row]
+        y1, last1 = R.gated_scan_forward(g[row], u[row], fl, h0[row], r)
+        d1 = R.gated_scan_backward(dy[row], g[row], u[row], y[row], fl, h0[row], r, dh[row])
+        torch.cuda.synchronize()
+        assert torch.equal(y[row], y1) and torch.equal(last[row], last1)
+        for name in ("dg", "du", "dh0"):
+            assert torch.equal(getattr(d, name)[row], getattr(d1, name)), name
+
+
 def test_other_stream_and_graph():
     say("scan on another stream and in a HIP graph")
     g, u, fl, h0, reset = case(2, 1500, 128, BF16, docs=3)
