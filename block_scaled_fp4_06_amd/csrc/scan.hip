@@ -10,7 +10,7 @@
 // Bound: HBM.  Forward reads g and u and writes y, 6 bytes per element in bf16; backward
 // reads dy, g, u, y and writes dg and du, 12 bytes.
 //
-//  * A tile is 128 bytes of channels (8 lanes of 16 bytes) by kTile time steps: each of 256
+//  * A tile is 128 bytes of channels (16 lanes of 8 bytes) by kTile time steps: each of 256
 //    threads holds kSteps consecutive steps of its channels in registers.  A run of steps
 //    acts on the state as h -> A h + B; the threads' (A, B) are composed through LDS.
 //  * The tiles of a sequence run in one kernel, so everything is read once.  A workgroup
@@ -27,46 +27,48 @@
 //
 // Few steps (up to kShort) need no tiles: a thread walks over them.
 //
-// Measured in bf16: forward with resets 8192 x 5120 in 77 us, 3.3 TB/s; backward with a
-// floor, 4 x 2048 x 5120, in 128 us, 3.9 TB/s (a copy reaches 5.1).  Without the exchange
-// between tiles they would take 70 and 125: the rest is one tile's way through load, LDS and
-// store, with 4 (backward 3) workgroups to a CU.  Longer runs per thread do not fit in
-// registers; tiles of 64 steps took 107 and 157 us, 4 workgroups backward 148.  One step
-// of 64 x 5120 takes 4.8 us.
+// Measured in bf16: forward with resets 8192 x 5120 in 75 us, 3.4 TB/s; backward with a
+// floor, 4 x 2048 x 5120, in 128 us, 3.9 TB/s (a copy reaches 5.1); without the exchange
+// between tiles 70 and 125.  The rest is one tile's way through load, LDS and store with 3
+// workgroups to a CU: 4 took 76 and 135 us, tiles of half the steps 107 and 157 us, and more
+// steps a thread do not fit in its registers.  16 bytes a lane, 4 steps: as fast, with twice
+// the LDS and 20 registers more.  One step of 64 x 5120 takes 3.7 us.
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kGroups = 32;          // time groups of a tile: 256 threads / 8 lanes of channels
-constexpr int kSteps = 4;            // steps of a thread
+constexpr int kWords = 2;            // words of an access
+constexpr int kLanes = 16;           // lanes of channels
+constexpr int kGroups = 256 / kLanes;   // time groups of a tile
+constexpr int kSteps = 8;            // steps of a thread
 constexpr int kTile = kGroups * kSteps;
-constexpr int kWindow = 4;           // tiles before its own that a tile looks at (1 to 8: alike here;
-                                     // few and long sequences gain from more than one)
+constexpr int kWindow = 8;           // tiles before its own that a tile looks at
+                                     // (65536 x 128: 1 tile 287 us, 2 156, 4 94, 8 65)
 constexpr int kLooks = 1 << 22;      // how often a tile looks before it gives up: seconds
 constexpr int kShort = 16;           // steps that one thread walks over by itself
 
 // ---------------------------------------------------------------- loads and stores
-// 16 bytes of channels, at any element's alignment (the packed type makes them single
+// 8 bytes of channels, at any element's alignment (the packed type makes them single
 // instructions).  PART: only `cnt` of the elements exist (fewer channels than one access
 // covers); otherwise a strip's last lanes take the last whole access, so that no load
 // depends on a branch, and store their own channels alone.
-struct __attribute__((packed, aligned(2))) Four { uint32_t w[4]; };
+struct __attribute__((packed, aligned(2))) Words { uint32_t w[kWords]; };
 
 template <bool F32>
 struct Raw {
-  static constexpr int V = F32 ? 4 : 8;
-  uint32_t w[4];
+  static constexpr int V = F32 ? kWords : 2 * kWords;
+  uint32_t w[kWords];
 
   template <bool PART>
   __device__ __forceinline__ void load(const char *p, int cnt) {
     if constexpr (!PART) {
-      const Four v = *reinterpret_cast<const Four *>(p);
+      const Words v = *reinterpret_cast<const Words *>(p);
 #pragma unroll
-      for (int l = 0; l < 4; ++l) w[l] = v.w[l];
+      for (int l = 0; l < kWords; ++l) w[l] = v.w[l];
     } else {
-      w[0] = w[1] = w[2] = w[3] = 0u;
+      for (int l = 0; l < kWords; ++l) w[l] = 0u;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if (j >= cnt) continue;
@@ -89,13 +91,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // Elements from .. to - 1 of the V at p; WHOLE: all of them.
 template <bool WHOLE, bool F32>
-__device__ __forceinline__ void store(char *p, int from, int to, const float (&v)[F32 ? 4 : 8]) {
-  constexpr int V = F32 ? 4 : 8;
+__device__ __forceinline__ void store(char *p, int from, int to, const float (&v)[F32 ? kWords : 2 * kWords]) {
+  constexpr int V = F32 ? kWords : 2 * kWords;
   if (WHOLE || (from <= 0 && to >= V)) {
-    Four f;
+    Words f;
 #pragma unroll
-    for (int l = 0; l < 4; ++l) f.w[l] = F32 ? __float_as_uint(v[l & 3]) : pack2(v[(2 * l) % V], v[(2 * l + 1) % V]);
-    *reinterpret_cast<Four *>(p) = f;
+    for (int l = 0; l < kWords; ++l) f.w[l] = F32 ? __float_as_uint(v[l % V]) : pack2(v[(2 * l) % V], v[(2 * l + 1) % V]);
+    *reinterpret_cast<Words *>(p) = f;
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -187,15 +189,15 @@ __device__ __forceinline__ void store_agent(uint64_t *p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Where a thread's V channels are: blockIdx.x counts strips of 8 V (y tiles, z batch rows).
+// Where a thread's V channels are: blockIdx.x counts strips of kLanes V (y tiles, z batch rows).
 // Its own are the elements own .. cnt - 1 of the access at col.
 template <int V, bool PART>
 struct Place {
   int64_t first, col;   // the strip's first channel; the thread's access
   int own, cnt;
   __device__ __forceinline__ explicit Place(int64_t chan) {
-    first = (int64_t)blockIdx.x * (8 * V);
-    col = first + (threadIdx.x & 7) * V;
+    first = (int64_t)blockIdx.x * (kLanes * V);
+    col = first + (threadIdx.x % kLanes) * V;
     own = 0;
     cnt = V;
     if constexpr (PART) {
@@ -207,7 +209,7 @@ struct Place {
   }
 };
 
-// The channel of a strip's place tid < 8 V (element tid % V of lane tid / V), whether there
+// The channel of a strip's place tid < kLanes V (element tid % V of lane tid / V), whether there
 // is one, and whether it is that lane's own.
 template <int V, bool PART>
 __device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t chan, bool &own) {
@@ -225,7 +227,7 @@ __device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t ch
 // Whether all of a tile's steps and of its strip's channels exist.
 template <int V>
 __device__ __forceinline__ bool whole_tile(const nvfp4_scan_args &a, int64_t j) {
-  return (j + 1) * kTile <= a.time && (int64_t)(blockIdx.x + 1) * (8 * V) <= a.chan;
+  return (j + 1) * kTile <= a.time && (int64_t)(blockIdx.x + 1) * (kLanes * V) <= a.chan;
 }
 
 // What the threads of a tile share.
@@ -242,7 +244,7 @@ struct Shared {
 // the pair of its segment's groups before it.
 template <int V, int CH>
 __device__ __forceinline__ void compose(Shared<CH> &sh, const Pair (&p)[V]) {
-  const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7;
+  const int tid = threadIdx.x, group = tid / kLanes, lane = tid % kLanes;
 #pragma unroll
   for (int i = 0; i < V; ++i) sh.group[group][lane * V + i] = p[i];
   __syncthreads();
@@ -300,11 +302,11 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
 // The state before each thread's steps from compose()'s result and the state before the
 // first tile (per channel).
 template <int V, bool PART>
-__device__ __forceinline__ void states_of_groups(Shared<8 * V> &sh, const Tiling &t, const float *given,
+__device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const Tiling &t, const float *given,
                                                  int64_t batch, int64_t j, int64_t first, int64_t chan,
                                                  float (&h)[V]) {
-  constexpr int CH = 8 * V, kSegs = Shared<CH>::kSegs;
-  const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7;
+  constexpr int CH = kLanes * V, kSegs = Shared<CH>::kSegs;
+  const int tid = threadIdx.x, group = tid / kLanes, lane = tid % kLanes;
   if (tid < 64) {
     Pair all = sh.seg[0][tid % CH];
 #pragma unroll
@@ -364,7 +366,7 @@ struct ForwardSteps {
   int64_t at, t0;   // the first one, and the first one read
   int more, last;   // how many there are; the last one read, from t0
   __device__ __forceinline__ ForwardSteps(int64_t j, int64_t time) {
-    at = j * kTile + (threadIdx.x >> 3) * kSteps;
+    at = j * kTile + (threadIdx.x / kLanes) * kSteps;
     t0 = WHOLE ? at : min(at, time - 1);
     more = WHOLE ? kSteps : (int)min((int64_t)kSteps, time - at);
     last = max(0, more - 1);
@@ -396,8 +398,8 @@ struct ForwardLoads {
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Tiling &tl, int64_t batch,
                                              int64_t j, const Place<Raw<F32>::V, PART> &pl,
-                                             ForwardLoads<F32, RESET> &in, Shared<8 * Raw<F32>::V> &sh) {
-  constexpr int V = Raw<F32>::V, CH = 8 * V;
+                                             ForwardLoads<F32, RESET> &in, Shared<kLanes * Raw<F32>::V> &sh) {
+  constexpr int V = Raw<F32>::V, CH = kLanes * V;
   Raw<F32>(&g)[kSteps] = in.g, (&u)[kSteps] = in.u;
   const ForwardSteps<WHOLE> st(j, a.time);
   float fl[V];
@@ -450,14 +452,14 @@ __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Til
 
 // (One branch for a workgroup: no lane of most tiles has anything to check.)
 template <bool F32, bool RESET, bool FLOOR, bool PART>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
   constexpr int V = Raw<F32>::V;
-  __shared__ Shared<8 * V> sh;
+  __shared__ Shared<kLanes * V> sh;
   const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
   const Place<V, PART> pl(a.chan);
   ForwardLoads<F32, RESET> in;
-  Taken<8 * V> taken;
+  Taken<kLanes * V> taken;
   taken.ask(tl, batch);
   int64_t j = guess;
   for (bool asked = false;;) {
@@ -541,7 +543,7 @@ struct BackwardSteps {
   int64_t steps, t0;       // how many from the first one on to the beginning; the first one read
   int more, last, prior;   // how many there are; the last one read, from t0; steps before t0
   __device__ __forceinline__ BackwardSteps(int64_t j, int64_t time) {
-    steps = time - (j * kTile + (threadIdx.x >> 3) * kSteps);
+    steps = time - (j * kTile + (threadIdx.x / kLanes) * kSteps);
     t0 = WHOLE ? steps - 1 : max((int64_t)0, steps - 1);
     more = WHOLE ? kSteps : (int)min((int64_t)kSteps, steps);
     last = max(0, more - 1);
@@ -589,11 +591,11 @@ struct BackwardLoads {
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling &tl, float *floors,
                                               int64_t batch, int64_t j, const Place<Raw<F32>::V, PART> &pl,
-                                              BackwardLoads<F32, RESET> &in, Shared<8 * Raw<F32>::V> &sh) {
-  constexpr int V = Raw<F32>::V, CH = 8 * V;
+                                              BackwardLoads<F32, RESET> &in, Shared<kLanes * Raw<F32>::V> &sh) {
+  constexpr int V = Raw<F32>::V, CH = kLanes * V;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
-  const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;
+  const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   Raw<F32>(&g)[kSteps] = in.g, (&dy)[kSteps] = in.dy, (&u)[kSteps] = in.u, (&y)[kSteps] = in.y;
   const BackwardSteps<WHOLE> st(j, a.time);
   float fl[V];
@@ -631,7 +633,7 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
 #pragma unroll
   for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(g[s].w[w]), "+v"(dy[s].w[w]));
+    for (int w = 0; w < kWords; ++w) asm volatile("" : "+v"(g[s].w[w]), "+v"(dy[s].w[w]));
   char *pdg = at<F32>(d.dg, batch * d.dg_batch + st.t0 * d.dg_time + pl.col);
   char *pdu = at<F32>(d.du, batch * d.du_batch + st.t0 * d.du_time + pl.col);
 #pragma unroll
@@ -677,11 +679,11 @@ template <bool F32, bool RESET, bool FLOOR, bool PART>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
   constexpr int V = Raw<F32>::V;
-  __shared__ Shared<8 * V> sh;
+  __shared__ Shared<kLanes * V> sh;
   const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
   const Place<V, PART> pl(l.a.chan);
   BackwardLoads<F32, RESET> in;
-  Taken<8 * V> taken;
+  Taken<kLanes * V> taken;
   taken.ask(tl, batch);
   auto whole = [&](int64_t j) { return !PART && j + 1 < tl.chunks && whole_tile<V>(l.a, j); };
   int64_t j = guess;
@@ -811,7 +813,7 @@ template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
   const hipError_t e = clear_words(l, s.ws, stream);
   if (e != hipSuccess) return e;
-  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, 8 * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
+  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, kLanes * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
     scan_forward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s.a, t);
   });
 }
@@ -820,7 +822,7 @@ template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
   const hipError_t e = clear_words(l, s.ws, stream);
   if (e != hipSuccess) return e;
-  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, 8 * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
+  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, kLanes * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
     scan_backward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s, t, floors);
   });
 }
@@ -837,7 +839,7 @@ hipError_t run_forward(const ScanLaunch &s, hipStream_t stream) {
     else scan_forward_short_kernel<F32, false><<<grid, 64, 0, stream>>>(a, threads);
     return hipGetLastError();
   }
-  const Layout l = layout_of(a.batch, a.time, a.chan, 8 * V, false);
+  const Layout l = layout_of(a.batch, a.time, a.chan, kLanes * V, false);
   if (few) return forward_tiles<F32, true, true, true>(s, l, stream);
   if (a.reset)
     return a.floor ? forward_tiles<F32, true, true, false>(s, l, stream)
@@ -851,7 +853,7 @@ hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
   constexpr int V = Raw<F32>::V;
   const nvfp4_scan_args &a = s.a;
   const bool few = a.chan < V;
-  const Layout l = layout_of(a.batch, a.time, a.chan, 8 * V, true);
+  const Layout l = layout_of(a.batch, a.time, a.chan, kLanes * V, true);
   float *floors = reinterpret_cast<float *>(static_cast<char *>(s.ws) + l.floors);
   hipError_t e = hipSuccess;
   if (a.batch > 0) {
@@ -882,8 +884,8 @@ hipError_t run_backward(const ScanLaunch &s, hipStream_t stream) {
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t batch, int64_t time, int64_t chan, bool backward) {
-  const size_t a = layout_of(batch, time, chan, 8 * Raw<false>::V, backward).bytes;
-  const size_t b = layout_of(batch, time, chan, 8 * Raw<true>::V, backward).bytes;
+  const size_t a = layout_of(batch, time, chan, kLanes * Raw<false>::V, backward).bytes;
+  const size_t b = layout_of(batch, time, chan, kLanes * Raw<true>::V, backward).bytes;
   return a > b ? a : b;   // (of either type)
 }
 
