@@ -367,7 +367,9 @@ __host__ __device__ inline Split split_rows(int64_t rows, int64_t groups, int st
     s.slots = want;
   } else {
     const int64_t per = rows / groups;
-    int64_t parts = (want + groups - 1) / groups;
+    // (rounded down: a few workgroups more than the CUs hold at once take twice as long)
+    int64_t parts = workgroups / groups * streams;
+    if (parts < streams) parts = streams;
     if (parts > per) parts = per;
     s.parts = (int)((parts + streams - 1) / streams * streams);   // (the last may be empty)
     s.slots = groups * s.parts;
