@@ -13,8 +13,8 @@
 // Work division: a workgroup takes one chunk of kAdamChunk elements of one tensor, found in
 // the table's running chunk counts; the launch covers every chunk of up to
 // kAdamGrads tensors, whose gradient pointers travel in the kernel's arguments.  (Chunks of
-// 2048, one pass of the workgroup in 8 bits: 60 tensors of 9 million elements in all take 30
-// us, 39 with 16384; the 30 small ones below 4.3 us, 5.1 with 4096, 11.4 with 16384.)
+// 4096: 60 tensors of 9 million elements in all take 31 us, 39 with 16384; 2048 lose 2 % on
+// large 8-bit tensors, the 30 small ones below take 5.1, 4.3 and with 16384 11.4 us.)
 //
 // 8-bit moments: a lane holds 8 consecutive elements, half a wave one block of 256; the
 // block's two largest magnitudes are maxima over 32 lanes.
@@ -23,7 +23,7 @@
 // 5.3-5.9 TB/s (a copy between two buffers: 5.1).  8-bit moments and stochastically rounded
 // bf16 weights 253-283 us a step, 3.7-4.2 TB/s: the rounds of Philox and the correctly
 // rounded roots and divisions bound it, not memory; both moments decoded to bf16 96 us, 6.6
-// TB/s (the codes were just written).  30 tensors of 60001 elements in all: 4.3 us.
+// TB/s (the codes were just written).  30 tensors of 60001 elements in all: 5.1 us.
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 

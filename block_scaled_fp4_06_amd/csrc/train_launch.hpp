@@ -43,7 +43,7 @@ hipError_t launch_scan_backward(const ScanLaunch &s, hipStream_t stream);
 
 // ---------------------------------------------------------------- AdamW
 // Elements of a tensor that one workgroup updates (a multiple of NVFP4_ADAMW_BLOCK).
-constexpr int kAdamChunk = 2048;
+constexpr int kAdamChunk = 4096;
 // Gradient pointers that travel with a launch, by value: 8 bytes each of the 4 KiB that a
 // kernel's arguments may take.
 constexpr int kAdamGrads = 440;
