@@ -289,8 +289,8 @@ const char *nvfp4_status_string(nvfp4_status s) {
   switch (v) {
     case NVFP4_OK: return "ok";
     case NVFP4_ERR_NULL: return "a required pointer is NULL";
-    case NVFP4_ERR_SHAPE: return "bad shape: sizes must be multiples of 16 and ld >= cols";
-    case NVFP4_ERR_ALIGN: return "pointer not 16-byte aligned or leading dimension not a multiple of 8";
+    case NVFP4_ERR_SHAPE: return "bad shape: a size, stride or leading dimension that the call does not take";
+    case NVFP4_ERR_ALIGN: return "pointer or leading dimension not aligned as the call needs it";
     case NVFP4_ERR_UNSUPPORTED: return "unsupported option combination";
     case NVFP4_ERR_WORKSPACE: return "workspace missing or too small";
     case NVFP4_ERR_HIP: return "HIP kernel launch failed";

@@ -370,7 +370,9 @@ nvfp4_status nvfp4_residual_norm_backward(const nvfp4_norm_params *p,
  * step with reset != 0, a_t = 0: h_t = u_t whatever came before (a document of a packed
  * row begins), also where what came before is inf or NaN.  y_t = h_t, rounded to the
  * tensor's type; the state itself is carried in binary32.  One step (time = 1) serves a
- * decoder; h_last may be h0 itself.
+ * decoder.  h_last may be h0 itself; no other output shares memory with an input.  The
+ * workspace (16-byte aligned, any contents) belongs to the call until the stream has
+ * passed it.  Results are the same bits every time.
  */
 typedef struct {            /* strides (*_batch, *_time) in elements; channels are contiguous */
     int64_t batch, time, chan;
