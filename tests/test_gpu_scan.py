@@ -311,6 +311,20 @@ def test_a_row_does_not_depend_on_the_others(b, t, c, dtype):
             assert torch.equal(getattr(d, name)[row], getattr(d1, name)), name
 
 
+def test_two_streams_at_once():
+    """Tiles of two calls share the GPU; each waits for its own call's tiles only."""
+    say("scan on two streams")
+    ins = [case(4, 3000, 640, BF16, docs=3, seed=k) for k in (1, 50)]
+    want = [R.gated_scan_forward(*i) for i in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [[R.gated_scan_forward(*i, stream=s) for i, s in zip(ins, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for (y, last), (y0, last0) in zip(turn, want):
+            assert torch.equal(y, y0) and torch.equal(last, last0)
+
+
 def test_other_stream_and_graph():
     say("scan on another stream and in a HIP graph")
     g, u, fl, h0, reset = case(2, 1500, 128, BF16, docs=3)
