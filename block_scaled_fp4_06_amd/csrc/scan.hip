@@ -27,12 +27,12 @@
 //
 // Few steps (up to kShort) need no tiles: a thread walks over them.
 //
-// Measured in bf16: forward with resets 8192 x 5120 in 75 us, 3.4 TB/s; backward with a
-// floor, 4 x 2048 x 5120, in 128 us, 3.9 TB/s (a copy reaches 5.1); without the exchange
-// between tiles 70 and 125.  The rest is one tile's way through load, LDS and store with 3
-// workgroups to a CU: 4 took 76 and 135 us, tiles of half the steps 107 and 157 us, and more
-// steps a thread do not fit in its registers.  16 bytes a lane, 4 steps: as fast, with twice
-// the LDS and 20 registers more.  One step of 64 x 5120 takes 3.7 us.
+// Measured in bf16: forward with resets 8192 x 5120 in 70 us, 3.6 TB/s; backward with a
+// floor, 4 x 2048 x 5120, in 114 us, 4.4 TB/s (a copy reaches 5.1); forward with a floor, 6 x
+// 800 x 8031, 52 us, 4.4 TB/s.  The rest is one tile's way through load, LDS, chain and store
+// with 3 workgroups to a CU: 4 gain nothing, tiles of half the steps took a third longer, and
+// more steps a thread do not fit in its registers.  16 bytes a lane, 4 steps: as fast, with
+// twice the LDS and 20 registers more.  One step of 64 x 5120 takes 3.7 us.
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 
@@ -164,9 +164,45 @@ __device__ __forceinline__ Pair then(const Pair &p, const Pair &q) {
 // the state after it as the pair that leads there from anywhere.  Zero: neither yet.
 struct Tiling {
   int64_t chunks;
-  int64_t chunk0, batch0;   // the launch's first tile and batch row (grids are bounded)
+  int64_t chunk0, strip0;   // the launch's first tile and strip (grids are bounded)
+  uint32_t across;          // strips of a batch row
+  uint32_t strips, each;    // the launch's strips; how many of them a die has at most (0: any die has any)
   uint32_t *taken;          // [strip][kLine]
   uint64_t *words;          // [strip][tile][place]
+};
+
+constexpr uint32_t kDies = 8;   // consecutive workgroups go to the dies in turn
+
+// The strip of a workgroup, and the tile that its place in the grid suggests.  A die gets a
+// run of strips: neighbouring ones share cache lines where rows do not begin at one.
+struct Spot {
+  int64_t strip, batch, tile;
+  int32_t at;   // the strip's place in its row
+  bool none;    // no strip: the dies' shares differ by one
+  __device__ __forceinline__ explicit Spot(const Tiling &t) {
+    const uint32_t n = blockIdx.x;
+    uint32_t k, turn;
+    none = false;
+    if (t.each) {
+      const uint32_t die = n % kDies, q = n / kDies;
+      const uint32_t from = (uint32_t)((uint64_t)die * t.strips / kDies), to = (uint32_t)((uint64_t)(die + 1) * t.strips / kDies);
+      turn = q / t.each;
+      k = from + (q - turn * t.each);
+      none = k >= to;
+    } else {
+      turn = n / t.strips;
+      k = n - turn * t.strips;
+    }
+    tile = t.chunk0 + turn;
+    strip = t.strip0 + k;
+    if (t.strip0 == 0) {   // (almost always: a division of 32 bits)
+      batch = k / t.across;
+      at = (int32_t)(k - (uint32_t)batch * t.across);
+    } else {
+      batch = strip / t.across;
+      at = (int32_t)(strip - batch * t.across);
+    }
+  }
 };
 
 constexpr int kLine = 32;   // (128 bytes: strips do not share lines)
@@ -189,14 +225,14 @@ __device__ __forceinline__ void store_agent(uint64_t *p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Where a thread's V channels are: blockIdx.x counts strips of kLanes V (y tiles, z batch rows).
+// Where a thread's V channels are, in the strip of kLanes V at `at`.
 // Its own are the elements own .. cnt - 1 of the access at col.
 template <int V, bool PART>
 struct Place {
   int64_t first, col;   // the strip's first channel; the thread's access
   int own, cnt;
-  __device__ __forceinline__ explicit Place(int64_t chan) {
-    first = (int64_t)blockIdx.x * (kLanes * V);
+  __device__ __forceinline__ Place(int64_t at, int64_t chan) {
+    first = at * (kLanes * V);
     col = first + (threadIdx.x % kLanes) * V;
     own = 0;
     cnt = V;
@@ -226,8 +262,8 @@ __device__ __forceinline__ int64_t channel_of(int tid, int64_t first, int64_t ch
 
 // Whether all of a tile's steps and of its strip's channels exist.
 template <int V>
-__device__ __forceinline__ bool whole_tile(const nvfp4_scan_args &a, int64_t j) {
-  return (j + 1) * kTile <= a.time && (int64_t)(blockIdx.x + 1) * (kLanes * V) <= a.chan;
+__device__ __forceinline__ bool whole_tile(const nvfp4_scan_args &a, int64_t j, int64_t first) {
+  return (j + 1) * kTile <= a.time && first + kLanes * V <= a.chan;
 }
 
 // What the threads of a tile share.
@@ -303,7 +339,7 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
 // first tile (per channel).
 template <int V, bool PART>
 __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const Tiling &t, const float *given,
-                                                 int64_t batch, int64_t j, int64_t first, int64_t chan,
+                                                 const Spot &at, int64_t j, int64_t first, int64_t chan,
                                                  float (&h)[V]) {
   constexpr int CH = kLanes * V, kSegs = Shared<CH>::kSegs;
   const int tid = threadIdx.x, group = tid / kLanes, lane = tid % kLanes;
@@ -315,10 +351,10 @@ __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const T
     if (j == 0 && given && tid < CH) {
       bool own;
       const int64_t c = channel_of<V, PART>(tid, first, chan, own);
-      if (!PART || own) before = given[batch * chan + c];
+      if (!PART || own) before = given[at.batch * chan + c];
       asm volatile("" : "+v"(before));   // (waits here, not behind the chain's stores)
     }
-    if (t.chunks > 1) before = state_before_tile<CH>(t, batch * gridDim.x + blockIdx.x, j, all, before);
+    if (t.chunks > 1) before = state_before_tile<CH>(t, at.strip, j, all, before);
     if (tid < CH) {
 #pragma unroll
       for (int s = 0; s < kSegs; ++s) {
@@ -339,9 +375,9 @@ __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const T
 template <int CH>
 struct Taken {
   uint32_t number = 0;
-  __device__ __forceinline__ void ask(const Tiling &t, int64_t batch) {
+  __device__ __forceinline__ void ask(const Tiling &t, int64_t strip) {
     if (t.chunks > 1 && threadIdx.x == 0)
-      number = __hip_atomic_fetch_add(t.taken + (batch * gridDim.x + blockIdx.x) * kLine, 1u,
+      number = __hip_atomic_fetch_add(t.taken + strip * kLine, 1u,
                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __device__ __forceinline__ int64_t tell(Shared<CH> &sh, const Tiling &t, int64_t guess) {
@@ -396,11 +432,12 @@ struct ForwardLoads {
 };
 
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
-__device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Tiling &tl, int64_t batch,
+__device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Tiling &tl, const Spot &spot,
                                              int64_t j, const Place<Raw<F32>::V, PART> &pl,
                                              ForwardLoads<F32, RESET> &in, Shared<kLanes * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = kLanes * V;
   Raw<F32>(&g)[kSteps] = in.g, (&u)[kSteps] = in.u;
+  const int64_t batch = spot.batch;
   const ForwardSteps<WHOLE> st(j, a.time);
   float fl[V];
   if constexpr (FLOOR) load_f32<V, PART>(a.floor, pl.col, pl.cnt, fl);
@@ -430,7 +467,7 @@ __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Til
   }
   compose<V, CH>(sh, p);
   float h[V];
-  states_of_groups<V, PART>(sh, tl, a.h0, batch, j, pl.first, a.chan, h);
+  states_of_groups<V, PART>(sh, tl, a.h0, spot, j, pl.first, a.chan, h);
   char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
@@ -456,11 +493,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
   constexpr int V = Raw<F32>::V;
   __shared__ Shared<kLanes * V> sh;
-  const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
-  const Place<V, PART> pl(a.chan);
+  const Spot at(tl);
+  if (at.none) return;
+  const int64_t batch = at.batch, guess = at.tile;
+  const Place<V, PART> pl(at.at, a.chan);
   ForwardLoads<F32, RESET> in;
   Taken<kLanes * V> taken;
-  taken.ask(tl, batch);
+  taken.ask(tl, at.strip);
   int64_t j = guess;
   for (bool asked = false;;) {
     in.template fetch<PART, false>(a, batch, j, pl);
@@ -470,10 +509,10 @@ void scan_forward_kernel(nvfp4_scan_args a, Tiling tl) {
     asked = true;
     j = mine;
   }
-  if (!PART && whole_tile<V>(a, j)) {
-    forward_tile<F32, RESET, FLOOR, PART, true>(a, tl, batch, j, pl, in, sh);
+  if (!PART && whole_tile<V>(a, j, pl.first)) {
+    forward_tile<F32, RESET, FLOOR, PART, true>(a, tl, at, j, pl, in, sh);
   } else {
-    forward_tile<F32, RESET, FLOOR, PART, false>(a, tl, batch, j, pl, in, sh);
+    forward_tile<F32, RESET, FLOOR, PART, false>(a, tl, at, j, pl, in, sh);
   }
 }
 
@@ -590,13 +629,14 @@ struct BackwardLoads {
 
 template <bool F32, bool RESET, bool FLOOR, bool PART, bool WHOLE>
 __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling &tl, float *floors,
-                                              int64_t batch, int64_t j, const Place<Raw<F32>::V, PART> &pl,
+                                              const Spot &spot, int64_t j, const Place<Raw<F32>::V, PART> &pl,
                                               BackwardLoads<F32, RESET> &in, Shared<kLanes * Raw<F32>::V> &sh) {
   constexpr int V = Raw<F32>::V, CH = kLanes * V;
   const nvfp4_scan_args &a = l.a;
   const nvfp4_scan_grads &d = l.d;
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   Raw<F32>(&g)[kSteps] = in.g, (&dy)[kSteps] = in.dy, (&u)[kSteps] = in.u, (&y)[kSteps] = in.y;
+  const int64_t batch = spot.batch;
   const BackwardSteps<WHOLE> st(j, a.time);
   float fl[V];
 #pragma unroll
@@ -628,7 +668,7 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
   in.template fetch_more<PART, WHOLE>(a, batch, st, pl);
   compose<V, CH>(sh, p);
   float c[V], dfl[V];
-  states_of_groups<V, PART>(sh, tl, d.dh_last, batch, j, pl.first, a.chan, c);
+  states_of_groups<V, PART>(sh, tl, d.dh_last, spot, j, pl.first, a.chan, c);
   // (the gates' sigmoids are formed again: kept, they would take 64 registers a thread)
 #pragma unroll
   for (int s = 0; s < kSteps; ++s)
@@ -680,12 +720,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
   constexpr int V = Raw<F32>::V;
   __shared__ Shared<kLanes * V> sh;
-  const int64_t batch = tl.batch0 + blockIdx.z, guess = tl.chunk0 + blockIdx.y;
-  const Place<V, PART> pl(l.a.chan);
+  const Spot at(tl);
+  if (at.none) return;
+  const int64_t batch = at.batch, guess = at.tile;
+  const Place<V, PART> pl(at.at, l.a.chan);
   BackwardLoads<F32, RESET> in;
   Taken<kLanes * V> taken;
-  taken.ask(tl, batch);
-  auto whole = [&](int64_t j) { return !PART && j + 1 < tl.chunks && whole_tile<V>(l.a, j); };
+  taken.ask(tl, at.strip);
+  auto whole = [&](int64_t j) { return !PART && j + 1 < tl.chunks && whole_tile<V>(l.a, j, pl.first); };
   int64_t j = guess;
   for (bool asked = false;;) {
     in.template fetch<PART, false>(l.a, l.d, batch, j, pl);
@@ -696,9 +738,9 @@ void scan_backward_kernel(ScanLaunch l, Tiling tl, float *floors) {
     j = mine;
   }
   if (whole(j)) {
-    backward_tile<F32, RESET, FLOOR, PART, true>(l, tl, floors, batch, j, pl, in, sh);
+    backward_tile<F32, RESET, FLOOR, PART, true>(l, tl, floors, at, j, pl, in, sh);
   } else {
-    backward_tile<F32, RESET, FLOOR, PART, false>(l, tl, floors, batch, j, pl, in, sh);
+    backward_tile<F32, RESET, FLOOR, PART, false>(l, tl, floors, at, j, pl, in, sh);
   }
 }
 
@@ -782,23 +824,31 @@ Layout layout_of(int64_t batch, int64_t time, int64_t chan, int place, bool back
 
 Tiling tiling_of(const Layout &l, void *ws) {
   char *p = static_cast<char *>(ws);
-  return Tiling{l.chunks, 0, 0, reinterpret_cast<uint32_t *>(p), reinterpret_cast<uint64_t *>(p + l.words)};
+  return Tiling{l.chunks, 0, 0, 0, 0, 0, reinterpret_cast<uint32_t *>(p), reinterpret_cast<uint64_t *>(p + l.words)};
 }
 
 uint32_t at_most(int64_t n, int64_t most) { return (uint32_t)(n < most ? n : most); }
 
-// Launches over all strips of `ch` channels, tiles and batch rows, the latter two in slices
-// that a grid can count.  launch(grid, tiling).
+// Launches over all strips of `ch` channels and their tiles, in slices that a grid can count.
+// Dies get runs of strips where that leaves none with much less than another (9 x 6143 x 468
+// backward 100 us, 119 without; 4 x 2048 x 5120, whose rows begin at cache lines, 120 and
+// 129).  launch(grid, tiling).
 template <class Launch>
-hipError_t over_tiles(const nvfp4_scan_args &a, Tiling t, int64_t chunks, int ch, Launch &&launch) {
-  constexpr int64_t most = 65535;
-  const uint32_t strips = (uint32_t)((a.chan + ch - 1) / ch);
-  for (t.batch0 = 0; t.batch0 < a.batch; t.batch0 += most)
-    for (t.chunk0 = 0; t.chunk0 < chunks; t.chunk0 += most) {
-      launch(dim3(strips, at_most(chunks - t.chunk0, most), at_most(a.batch - t.batch0, most)), t);
+hipError_t over_tiles(const nvfp4_scan_args &a, Tiling t, int ch, Launch &&launch) {
+  constexpr int64_t most = 1 << 20, grid = 1 << 23;
+  t.across = (uint32_t)((a.chan + ch - 1) / ch);
+  const int64_t strips = a.batch * t.across;
+  for (; t.strip0 < strips; t.strip0 += most) {
+    t.strips = at_most(strips - t.strip0, most);
+    t.each = (t.strips + kDies - 1) / kDies;
+    if (t.each * kDies > t.strips + t.strips / 8) t.each = 0;
+    const int64_t row = t.each ? t.each * kDies : t.strips, turns = grid / row;
+    for (t.chunk0 = 0; t.chunk0 < t.chunks; t.chunk0 += turns) {
+      launch((uint32_t)(row * at_most(t.chunks - t.chunk0, turns)), t);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
+  }
   return hipSuccess;
 }
 
@@ -813,7 +863,7 @@ template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t forward_tiles(const ScanLaunch &s, const Layout &l, hipStream_t stream) {
   const hipError_t e = clear_words(l, s.ws, stream);
   if (e != hipSuccess) return e;
-  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, kLanes * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
+  return over_tiles(s.a, tiling_of(l, s.ws), kLanes * Raw<F32>::V, [&](uint32_t grid, const Tiling &t) {
     scan_forward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s.a, t);
   });
 }
@@ -822,7 +872,7 @@ template <bool F32, bool RESET, bool FLOOR, bool PART>
 hipError_t backward_tiles(const ScanLaunch &s, const Layout &l, float *floors, hipStream_t stream) {
   const hipError_t e = clear_words(l, s.ws, stream);
   if (e != hipSuccess) return e;
-  return over_tiles(s.a, tiling_of(l, s.ws), l.chunks, kLanes * Raw<F32>::V, [&](dim3 grid, const Tiling &t) {
+  return over_tiles(s.a, tiling_of(l, s.ws), kLanes * Raw<F32>::V, [&](uint32_t grid, const Tiling &t) {
     scan_backward_kernel<F32, RESET, FLOOR, PART><<<grid, 256, 0, stream>>>(s, t, floors);
   });
 }
