@@ -129,15 +129,14 @@ class AdamW:
         if s.master is not None:
             N._check_buffer("state.master", s.master, (end,), (torch.float32,), self.device, False)
 
-    def _layout(self, grads):
+    def _layout(self, kinds):
         """The table of tensors for gradients of these types, on the host and the device; made
         again when a parameter's storage, the state or a gradient's type has changed."""
         import torch
         s = self.state
-        pins = [p.data_ptr() for p in self.params]
+        pins = list(map(torch.Tensor.data_ptr, self.params))
         pins += [t.data_ptr() for t in (s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
                                         s.exp_avg_sq_scale, s.master) if t is not None]
-        kinds = [p.dtype if g is None else g.dtype for g, p in zip(grads, self.params)]
         if self._table is not None and self._table[0] == pins and self._table[1] == kinds:
             return self._table
         self._check_state()
@@ -164,9 +163,19 @@ class AdamW:
         return self._table
 
     def _check_grads(self, grads):
-        """One gradient (or None) per parameter: contiguous, of its shape, on its device."""
+        """(pointers, types) of one gradient (or None) per parameter: contiguous, of its shape,
+        on its device."""
         import torch
-        dev, kinds = self.device, (torch.bfloat16, torch.float32)
+        dev, kinds, each = self.device, (torch.bfloat16, torch.float32), torch.Tensor
+        # all at once where all are there and right; otherwise one by one, to say which is not
+        try:
+            types = [g.dtype for g in grads]
+            if (all(map(each.is_contiguous, grads)) and set(types).issubset(kinds) and
+                    list(map(each.size, grads)) == self._shapes and
+                    set(map(each.get_device, grads)) == {dev.index}):
+                return list(map(each.data_ptr, grads)), types
+        except (AttributeError, TypeError):
+            pass
         for i, (g, shape) in enumerate(zip(grads, self._shapes)):
             if g is None:
                 continue
@@ -178,6 +187,8 @@ class AdamW:
                                  "torch.float32" % (i, g.dtype))
             if g.device != dev:
                 raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
+        return ([0 if g is None else g.data_ptr() for g in grads],
+                [p.dtype if g is None else g.dtype for g, p in zip(grads, self.params)])
 
     def step(self, grads=None, lr=None, grad_scale=None, stream=None):
         """One update.  grads: a list like params (default: each parameter's .grad), contiguous,
@@ -190,8 +201,7 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
         dev, f32 = self.device, torch.float32
-        self._check_grads(grads)
-        pointers = [0 if g is None else g.data_ptr() for g in grads]
+        pointers, kinds = self._check_grads(grads)
         if grad_scale is not None:
             N._check_buffer("grad_scale", grad_scale.reshape(-1), (1,), (f32,), dev, False)
         if lr is not None:
@@ -201,7 +211,7 @@ class AdamW:
                                           s.exp_avg_scale, s.exp_avg_sq_scale, s.master)
 
         def call(handle):
-            _, _, host, device = self._layout(grads)
+            _, _, host, device = self._layout(kinds)
             prm = N.AdamWParams(self.lr, self.betas[0], self.betas[1], self.eps, s.step + 1,
                                 self.seed, 1 if self.stochastic_rounding else 0, 0,
                                 ptr(grad_scale))
