@@ -31,44 +31,53 @@ class GatedScanGrads:
     dfloor: Optional["object"]
 
 
-def _sequence(name, t, like):
-    if t.shape != like.shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
-                                                           tuple(like.shape)))
-    if t.dtype is not like.dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
-    if t.device != like.device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
-    batch, time, chan = t.shape
-    if not t.is_contiguous() and t.numel() and (
-            (chan > 1 and t.stride(2) != 1) or (time > 1 and t.stride(1) < chan)):
+def _sequence(name, t, shape, dtype, device):
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype is not dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    _steps(name, t, shape)
+
+
+def _steps(name, t, shape):
+    if t.is_contiguous() or not t.numel():
+        return
+    _, time, chan = shape
+    if (chan > 1 and t.stride(2) != 1) or (time > 1 and t.stride(1) < chan):
         raise ValueError("%s must have unit channel stride and time steps apart" % name)
 
 
-def _state(name, t, shape, like):
-    import torch
-    if t is None:
-        return
-    N._check_buffer(name, t, shape, (torch.float32,), like.device, False)
+def _plain(name, t, shape, dtypes, device):
+    if t is not None and (t.shape != shape or t.dtype not in dtypes or t.device != device or
+                          not t.is_contiguous()):
+        N._check_buffer(name, t, shape, dtypes, device, False)   # (says what is wrong)
 
 
 def _check_inputs(g, u, floor, h0, reset):
+    """The shape, type and device that the other tensors share with g."""
     import torch
     if g.dim() != 3:
         raise ValueError("g must be (batch, time, chan), not %d-D" % g.dim())
     dtype_code("g", g)
-    _sequence("g", g, g)
-    _sequence("u", u, g)
-    batch, time, chan = g.shape
-    _state("floor", floor, (chan,), g)
-    _state("h0", h0, (batch, chan), g)
-    if reset is not None:
-        N._check_buffer("reset", reset, (batch, time), (torch.bool, torch.uint8), g.device, False)
+    shape, dtype, device = g.shape, g.dtype, g.device
+    _steps("g", g, shape)
+    _sequence("u", u, shape, dtype, device)
+    batch, time, chan = shape
+    f32 = (torch.float32,)
+    _plain("floor", floor, (chan,), f32, device)
+    _plain("h0", h0, (batch, chan), f32, device)
+    _plain("reset", reset, (batch, time), (torch.bool, torch.uint8), device)
+    return shape, dtype, device
 
 
 def _strides(t):
-    batch, time, _ = t.shape
-    b, t, _ = t.stride()
+    batch, time, chan = t.shape
+    if t.is_contiguous():
+        b, t = time * chan, chan
+    else:
+        b, t, _ = t.stride()
     return (b if batch > 1 else 0), (t if time > 1 else 0)
 
 
@@ -83,10 +92,9 @@ def gated_scan_forward(g, u, floor=None, h0=None, reset=None, h_last=None, strea
     """(y, h_last): every step's state in the type of g, and the last one in float32 (into
     h_last where given; h0 itself for a state kept in place)."""
     import torch
-    _check_inputs(g, u, floor, h0, reset)
-    batch, time, chan = g.shape
-    _state("h_last", h_last, (batch, chan), g)
-    dev, given = g.device, h_last
+    (batch, time, chan), _, dev = _check_inputs(g, u, floor, h0, reset)
+    _plain("h_last", h_last, (batch, chan), (torch.float32,), dev)
+    given = h_last
 
     def call(handle):
         y = new_like(g)
@@ -110,15 +118,14 @@ def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=No
     u may be (the two halves of one projection's gradient, for example); neither may share
     memory with an input."""
     import torch
-    _check_inputs(g, u, floor, h0, reset)
-    _sequence("dy", dy, g)
-    _sequence("y", y, g)
-    batch, time, chan = g.shape
-    _state("dh_last", dh_last, (batch, chan), g)
+    shape, dtype, dev = _check_inputs(g, u, floor, h0, reset)
+    _sequence("dy", dy, shape, dtype, dev)
+    _sequence("y", y, shape, dtype, dev)
+    batch, time, chan = shape
+    _plain("dh_last", dh_last, (batch, chan), (torch.float32,), dev)
     if out is not None:
-        _sequence("out[0]", out[0], g)
-        _sequence("out[1]", out[1], g)
-    dev = g.device
+        _sequence("out[0]", out[0], shape, dtype, dev)
+        _sequence("out[1]", out[1], shape, dtype, dev)
 
     def call(handle):
         dg, du = (new_like(g), new_like(g)) if out is None else out
