@@ -20,7 +20,7 @@ repeat that step's values.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
 from dataclasses import dataclass
 from typing import Optional
 
@@ -173,7 +173,7 @@ class AdamW:
             if (all(map(each.is_contiguous, grads)) and set(types).issubset(kinds) and
                     list(map(each.size, grads)) == self._shapes and
                     set(map(each.get_device, grads)) == {dev.index}):
-                return list(map(each.data_ptr, grads)), types
+                return array("Q", map(each.data_ptr, grads)), types
         except (AttributeError, TypeError):
             pass
         for i, (g, shape) in enumerate(zip(grads, self._shapes)):
@@ -187,7 +187,7 @@ class AdamW:
                                  "torch.float32" % (i, g.dtype))
             if g.device != dev:
                 raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
-        return ([0 if g is None else g.data_ptr() for g in grads],
+        return (array("Q", [0 if g is None else g.data_ptr() for g in grads]),
                 [p.dtype if g is None else g.dtype for g, p in zip(grads, self.params)])
 
     def step(self, grads=None, lr=None, grad_scale=None, stream=None):
@@ -216,7 +216,7 @@ class AdamW:
                                 self.seed, 1 if self.stochastic_rounding else 0, 0,
                                 ptr(grad_scale))
             check(N.nvfp4_adamw_step(host.data_ptr(), device.data_ptr(),
-                                     (ctypes.c_void_p * len(pointers))(*pointers), prm, handle),
+                                     pointers.buffer_info()[0], prm, handle),
                   "nvfp4_adamw_step")
             if stream is not None:   # (the table may be remade before this stream has passed)
                 device.record_stream(stream)
