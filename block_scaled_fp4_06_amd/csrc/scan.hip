@@ -27,8 +27,8 @@
 //
 // Few steps (up to kShort) need no tiles: a thread walks over them.
 //
-// Measured in bf16: forward with resets 8192 x 5120 in 70 us, 3.6 TB/s; backward with a
-// floor, 4 x 2048 x 5120, in 114 us, 4.4 TB/s (a copy reaches 5.1); forward with a floor, 6 x
+// Measured in bf16: forward with resets 8192 x 5120 in 68 us, 3.7 TB/s; backward with a
+// floor, 4 x 2048 x 5120, in 113 us, 4.5 TB/s (a copy reaches 5.1); forward with a floor, 6 x
 // 800 x 8031, 52 us, 4.4 TB/s.  The rest is one tile's way through load, LDS, chain and store
 // with 3 workgroups to a CU: 4 gain nothing, tiles of half the steps took a third longer, and
 // more steps a thread do not fit in its registers.  16 bytes a lane, 4 steps: as fast, with
@@ -44,8 +44,9 @@ constexpr int kLanes = 16;           // lanes of channels
 constexpr int kGroups = 256 / kLanes;   // time groups of a tile
 constexpr int kSteps = 8;            // steps of a thread
 constexpr int kTile = kGroups * kSteps;
-constexpr int kWindow = 8;           // tiles before its own that a tile looks at
-                                     // (65536 x 128: 1 tile 287 us, 2 156, 4 94, 8 65)
+constexpr int kFirst = 1;            // tiles before its own that a tile looks at first
+constexpr int kWindow = 8;           // ... and while it waits (65536 x 128: 1 tile 287 us, 2 156,
+                                     // 4 94, 8 61, 16 49, but 8192 x 5120 with 16 70, with 8 68)
 constexpr int kLooks = 1 << 22;      // how often a tile looks before it gives up: seconds
 constexpr int kShort = 16;           // steps that one thread walks over by itself
 
@@ -296,6 +297,25 @@ __device__ __forceinline__ void compose(Shared<CH> &sh, const Pair (&p)[V]) {
   __syncthreads();
 }
 
+// The state before tile j > 0 (whose words are at `own`) as far as it follows from the W tiles
+// before: whether it does in all lanes.
+template <int CH, int W>
+__device__ __forceinline__ bool look(const uint64_t *own, int64_t j, float &before) {
+  const int reach = (int)min((int64_t)W, j);
+  uint64_t w[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) w[k] = load_agent(own - (int64_t)min(k + 1, reach) * CH);
+  // from the nearest state on (which needs none before it)
+  bool gap = true;
+#pragma unroll
+  for (int k = W - 1; k >= 0; --k) {
+    const Pair p = pair_of(w[k]);
+    gap = w[k] == 0ull || (gap && !is_cut(p.a));
+    before = apply(p, before);
+  }
+  return !__any(gap);
+}
+
 // The chain.  In wave 0, lane = place: from the tile's pair to the state before it, and what
 // other tiles need to know of both.  `given` is the state before the first tile.  States
 // follow from the one before by one pair, in order, however many of those a tile applies
@@ -307,28 +327,16 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
   uint64_t *own = t.words + (strip * t.chunks + j) * CH + threadIdx.x % CH;
   float before = given;
   if (j > 0) {
-    bool told = !more;   // (a pair is only for those who wait with this tile)
-    const int reach = (int)min((int64_t)kWindow, j);
-    for (int looks = 0;; ++looks) {
-      uint64_t w[kWindow];
-#pragma unroll
-      for (int k = 0; k < kWindow; ++k) w[k] = load_agent(own - (int64_t)min(k + 1, reach) * CH);
-      // from the nearest state on (which needs none before it)
-      bool gap = true;
-#pragma unroll
-      for (int k = kWindow - 1; k >= 0; --k) {
-        const Pair p = pair_of(w[k]);
-        gap = w[k] == 0ull || (gap && !is_cut(p.a));
-        before = apply(p, before);
+    if (!look<CH, kFirst>(own, j, before)) {
+      if (live && more) store_agent(own, word_of(all));   // (a pair is for those who wait with this tile)
+      int looks = 0;
+      while (!look<CH, kWindow>(own, j, before)) {
+        if (++looks == kLooks) {   // (never: see the order of the tiles)
+          before = __uint_as_float(0x7FC00000u);
+          break;
+        }
+        __builtin_amdgcn_s_sleep(1);
       }
-      if (!__any(gap)) break;
-      if (!told && live) store_agent(own, word_of(all));
-      told = true;
-      if (looks == kLooks) {   // (never: see the order of the tiles)
-        before = __uint_as_float(0x7FC00000u);
-        break;
-      }
-      __builtin_amdgcn_s_sleep(1);
     }
   }
   if (live && more) store_agent(own, word_of(Pair{cut_mark(), apply(all, before)}));
