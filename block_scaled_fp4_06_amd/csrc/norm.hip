@@ -28,8 +28,8 @@
 //    strips of columns that walk down the rows.
 //
 // Measured at 8192 x 5120 (bf16, fp32 weights, one gate row): forward 66 us, 5.1 TB/s, the
-// rate of a copy; backward 112-118 us, 4.3-4.5 TB/s, of which the sums over rows take 5.
-// 2048 x 20480, two passes backward: 88 and 207 us.  One row of 5120: 4 us.
+// rate of a copy; backward 115 us, 4.4 TB/s, of which the sums over rows take 5.
+// 2048 x 20480, two passes backward: 88 and 205 us.  One row of 5120: 4 us.
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 
@@ -409,6 +409,7 @@ template <bool XF, bool ZF>
 struct Operands {         // one row's
   Raw<XF> x, d;
   Raw<ZF> z, h;
+  float r, rp;            // rstd and rstd_post
   // Makes the compiler unpack the words again where they are used next, instead of keeping
   // 32 unpacked values across the row's reduction.
   __device__ __forceinline__ void unpack_again() {
@@ -428,6 +429,8 @@ template <bool PART, bool XF, bool ZF>
 __device__ __forceinline__ void fetch_row(const nvfp4_norm_backward_args &a, int64_t row,
                                           const Place<PART> &at, Operands<XF, ZF> &o) {
   o.d.zero(); o.z.zero(); o.h.zero();
+  o.r = a.next_weight ? a.rstd[row] : 0.0f;
+  o.rp = a.z ? a.rstd_post[row] : 0.0f;
   fetch<PART>(a.x_out, row * a.ld_x_out + at.col, at.cnt, o.x);
   if (a.z) fetch<PART>(a.z, row * a.ld_z + at.col, at.cnt, o.z);
   if (a.dx_out) fetch<PART>(a.dx_out, row * a.ld_dx_out + at.col, at.cnt, o.d);
@@ -494,13 +497,12 @@ __device__ __forceinline__ void close_group(const NormBackward &b, const Split &
 // A thread's share of three sums over a row: t x, G z (dx_out + rstd t) and G z x with
 // t = dh (c + next); their factors rstd and rstd_post are the row's.
 template <bool XF, bool ZF>
-__device__ __forceinline__ void partial_sums(const Operands<XF, ZF> &o, const Columns &c, float r,
-                                             float (&s)[3]) {
+__device__ __forceinline__ void partial_sums(const Operands<XF, ZF> &o, const Columns &c, float (&s)[3]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x = o.x.get(j), t = o.h.get(j) * c.wn[j], q = c.g[j] * o.z.get(j);
     s[0] = __builtin_fmaf(t, x, s[0]);
-    s[1] = __builtin_fmaf(q, __builtin_fmaf(r, t, o.d.get(j)), s[1]);
+    s[1] = __builtin_fmaf(q, __builtin_fmaf(o.r, t, o.d.get(j)), s[1]);
     s[2] = __builtin_fmaf(q, x, s[2]);
   }
 }
@@ -514,8 +516,8 @@ __device__ __forceinline__ void means_of(const float (&s)[3], float r, float rp,
 // dx and dz of one row, and its terms of the sums over rows.
 template <bool PART, bool XF, bool ZF>
 __device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, const Operands<XF, ZF> &o,
-                                           const Place<PART> &at, float r, float rp, float m1, float m2,
-                                           Columns &c) {
+                                           const Place<PART> &at, float m1, float m2, Columns &c) {
+  const float r = o.r, rp = o.rp;
   const float skip = b.a.z ? b.p.skip_scale : 1.0f, k1 = -r * m1, k2 = -rp * m2;
   float dx[8], dz[8];
 #pragma unroll
@@ -599,7 +601,8 @@ __device__ __forceinline__ void close_slots(const NormBackward &b, const Split &
 // blockDim = (64 waves, streams): R rows per stream at a time, whose sums share one
 // reduction.  THREADS bounds the workgroup: fewer threads leave more registers to each.
 // What keeps it from a copy's rate is a row's way through the reduction with one workgroup
-// to a CU; two rows at a time took 8192 x 5120 from 131 to 121 us, and registers for a
+// to a CU; two rows at a time took 8192 x 5120 from 131 to 121 us, rstd fetched
+// ahead with its row from 119 to 115 (16384 x 2560 from 127 to 110), and registers for a
 // second workgroup spill (247 us).
 template <bool XF, bool ZF, int THREADS, int R, bool ONE, bool PART>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, Split sp) {
@@ -622,13 +625,11 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, 
   Columns c;
   walk_rows<R, ONE, PART, XF, ZF>(b, sp, row, end, count, at, c,
                                   [&](const int64_t (&rows)[R], const bool (&live)[R], Operands<XF, ZF> (&o)[R]) {
-    float r[R], rp[R], s[3 * R];
+    float s[3 * R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      r[k] = b.a.next_weight ? b.a.rstd[rows[k]] : 0.0f;
-      rp[k] = b.a.z ? b.a.rstd_post[rows[k]] : 0.0f;
       float t[3] = {0.0f, 0.0f, 0.0f};
-      partial_sums(o[k], c, r[k], t);
+      partial_sums(o[k], c, t);
 #pragma unroll
       for (int i = 0; i < 3; ++i) s[3 * k + i] = t[i];
     }
@@ -637,16 +638,16 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, 
     for (int k = 0; k < R; ++k) {
       const float t[3] = {s[3 * k], s[3 * k + 1], s[3 * k + 2]};
       float m1, m2;
-      means_of(t, r[k], rp[k], scale, m1, m2);
+      means_of(t, o[k].r, o[k].rp, scale, m1, m2);
       o[k].unpack_again();
-      if (live[k]) finish_row(b, rows[k], o[k], at, r[k], rp[k], m1, m2, c);
+      if (live[k]) finish_row(b, rows[k], o[k], at, m1, m2, c);
     }
   });
   close_slots(b, sp, blockIdx.x, at, c, lds);
 }
 
 // Long rows, first pass: m1 and m2 of every row, a workgroup per row at a time.  (HBM; both
-// passes read everything, so 20 of 12 bytes an element: 207 us at 2048 x 20480.)
+// passes read everything, 20 bytes an element where one pass has 12: 205 us at 2048 x 20480.)
 template <bool XF, bool ZF>
 __global__ __launch_bounds__(512) void norm_means_kernel(NormBackward b, float *means) {
   __shared__ float part[2][16][3];
@@ -655,15 +656,16 @@ __global__ __launch_bounds__(512) void norm_means_kernel(NormBackward b, float *
   const float scale = 1.0f / (float)cols;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < b.p.rows; row += gridDim.x) {
-    const float r = b.a.next_weight ? b.a.rstd[row] : 0.0f, rp = b.a.z ? b.a.rstd_post[row] : 0.0f;
-    float s[3] = {0.0f, 0.0f, 0.0f};
+    float s[3] = {0.0f, 0.0f, 0.0f}, r = 0.0f, rp = 0.0f;
     for (int col = (int)threadIdx.x * 8; col < cols; col += (int)blockDim.x * 8) {
       const Place<false> at(col, cols);
       Operands<XF, ZF> o;
       fetch_row(b.a, row, at, o);
       Columns c;
       open_slot(b, row / per, at, c);
-      partial_sums(o, c, r, s);
+      partial_sums(o, c, s);
+      r = o.r;
+      rp = o.rp;
     }
     row_sum<3>(s, part, turn, waves);
     if (threadIdx.x == 0) means_of(s, r, rp, scale, means[2 * row], means[2 * row + 1]);
@@ -682,8 +684,7 @@ __global__ __launch_bounds__(256) void norm_strips_kernel(NormBackward b, Split 
   walk_rows<1, false, false, XF, ZF>(b, sp, row, end, end - row, at, c,
                                      [&](const int64_t (&rows)[1], const bool (&)[1], Operands<XF, ZF> (&o)[1]) {
     const int64_t i = rows[0];
-    const float r = b.a.next_weight ? b.a.rstd[i] : 0.0f, rp = b.a.z ? b.a.rstd_post[i] : 0.0f;
-    finish_row(b, i, o[0], at, r, rp, means[2 * i], means[2 * i + 1], c);
+    finish_row(b, i, o[0], at, means[2 * i], means[2 * i + 1], c);
   });
   close_slots(b, sp, slot, at, c, nullptr);   // (one stream)
 }
