@@ -30,6 +30,7 @@
 // Measured at 8192 x 5120 (bf16, fp32 weights, one gate row): forward 66 us, 5.1 TB/s, the
 // rate of a copy; backward 115 us, 4.4 TB/s, of which the sums over rows take 5.
 // 2048 x 20480, two passes backward: 88 and 205 us.  One row of 5120: 4 us.
+#include "norm_rows.hpp"
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
 
@@ -354,50 +355,6 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormForward n) {
 // ---------------------------------------------------------------- backward
 constexpr int kMaxRow = 8192;     // columns of a row that one workgroup holds: 1024 x 8
 
-// How the rows are shared out among slots, ranges of rows that one workgroup or one of its
-// `streams` walks over.  A slot has whole groups (rows that share a gate row), or, where
-// groups are fewer than the slots wanted, an even part of one group; the streams of a
-// workgroup then have parts of the same group.
-struct Split {
-  int64_t rows, groups, slots;
-  int parts;        // slots per group; 0: a slot has whole groups
-  int streams;      // slots per workgroup, whose sums leave it as one
-  int64_t sums;     // workgroups: rows of each result's sums in the workspace
-};
-
-__host__ __device__ inline Split split_rows(int64_t rows, int64_t groups, int streams, int64_t workgroups) {
-  Split s = {rows, groups, 0, 0, streams, 0};
-  int64_t want = workgroups * streams;
-  if (want > rows) want = rows;
-  if (groups >= want) {
-    s.slots = want;
-  } else {
-    const int64_t per = rows / groups;
-    // (rounded down: a few workgroups more than the CUs hold at once take twice as long)
-    int64_t parts = workgroups / groups * streams;
-    if (parts < streams) parts = streams;
-    if (parts > per) parts = per;
-    s.parts = (int)((parts + streams - 1) / streams * streams);   // (the last may be empty)
-    s.slots = groups * s.parts;
-  }
-  s.sums = (s.slots + streams - 1) / streams;
-  return s;
-}
-
-__device__ __forceinline__ void slot_rows(const Split &s, int64_t slot, int64_t &r0, int64_t &r1) {
-  const int64_t per = s.rows / s.groups;
-  if (slot >= s.slots) {
-    r0 = r1 = s.rows;
-  } else if (s.parts == 0) {
-    r0 = slot * s.groups / s.slots * per;
-    r1 = (slot + 1) * s.groups / s.slots * per;
-  } else {
-    const int64_t g = slot / s.parts, i = slot % s.parts;
-    r0 = g * per + i * per / s.parts;
-    r1 = g * per + (i + 1) * per / s.parts;
-  }
-}
-
 // What a thread keeps for its columns: c + next; G = branch gate (c + post) of the current
 // group; and the sums over rows.
 struct Columns {
@@ -479,7 +436,7 @@ __device__ __forceinline__ void open_slot(const NormBackward &b, int64_t group, 
 }
 
 // The end of a group: s goes into dpost and, where the group was the slot's alone, the
-// gate's gradient (a part of a group leaves its s for close_slot).
+// gate's gradient (a part of a group leaves its s for close_slots).
 template <bool PART>
 __device__ __forceinline__ void close_group(const NormBackward &b, const Split &s, int64_t group,
                                             const Place<PART> &at, Columns &c) {
@@ -545,6 +502,7 @@ __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp
   static_assert(ONE || R == 1, "groups may end after any row");
   const int64_t per = sp.rows / sp.groups, last = max((int64_t)0, min(end, sp.rows) - 1);
   int64_t group = min(row, last) / per, left = (group + 1) * per - row;   // rows of the group from here on
+  const bool closes = closes_group(row, end);
   open_slot(b, group, at, c);
   Operands<XF, ZF> o[R], ahead[R];
 #pragma unroll
@@ -570,7 +528,7 @@ __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp
       }
     }
   }
-  if (ONE) close_group(b, sp, group, at, c);
+  if (ONE && closes) close_group(b, sp, group, at, c);
 }
 
 // The sums of a workgroup's streams, added in order through LDS, into the workspace.  (A
