@@ -319,10 +319,13 @@ __device__ __forceinline__ bool look(const uint64_t *own, int64_t j, float &befo
 // The chain.  In wave 0, lane = place: from the tile's pair to the state before it, and what
 // other tiles need to know of both.  `given` is the state before the first tile.  States
 // follow from the one before by one pair, in order, however many of those a tile applies
-// itself: results do not depend on who was first.
+// itself: results do not depend on who was first.  `in_place`: the state after the last tile
+// takes the place of the one before the first, so the last tile also waits for the first one's
+// word, which that tells only when it has read the state (behind a cut, nothing else would
+// make it wait for that).
 template <int CH>
 __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t strip, int64_t j, const Pair &all,
-                                                   float given) {
+                                                   float given, bool in_place) {
   const bool live = threadIdx.x < CH, more = j + 1 < t.chunks;
   uint64_t *own = t.words + (strip * t.chunks + j) * CH + threadIdx.x % CH;
   float before = given;
@@ -339,6 +342,14 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
       }
     }
   }
+  if (in_place && !more && j > 0) {
+    const uint64_t *first = own - j * CH;
+    for (int looks = 0; __any(load_agent(first) == 0ull); __builtin_amdgcn_s_sleep(1))
+      if (++looks == kLooks) {   // (never, as above)
+        before = __uint_as_float(0x7FC00000u);
+        break;
+      }
+  }
   if (live && more) store_agent(own, word_of(Pair{cut_mark(), apply(all, before)}));
   return before;
 }
@@ -348,7 +359,7 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
 template <int V, bool PART>
 __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const Tiling &t, const float *given,
                                                  const Spot &at, int64_t j, int64_t first, int64_t chan,
-                                                 float (&h)[V]) {
+                                                 float (&h)[V], bool in_place = false) {
   constexpr int CH = kLanes * V, kSegs = Shared<CH>::kSegs;
   const int tid = threadIdx.x, group = tid / kLanes, lane = tid % kLanes;
   if (tid < 64) {
@@ -360,9 +371,9 @@ __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const T
       bool own;
       const int64_t c = channel_of<V, PART>(tid, first, chan, own);
       if (!PART || own) before = given[at.batch * chan + c];
-      asm volatile("" : "+v"(before));   // (waits here, not behind the chain's stores)
+      asm volatile("" : "+v"(before) : : "memory");   // (waits here: the chain's stores come after)
     }
-    if (t.chunks > 1) before = state_before_tile<CH>(t, at.strip, j, all, before);
+    if (t.chunks > 1) before = state_before_tile<CH>(t, at.strip, j, all, before, in_place);
     if (tid < CH) {
 #pragma unroll
       for (int s = 0; s < kSegs; ++s) {
@@ -475,7 +486,7 @@ __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Til
   }
   compose<V, CH>(sh, p);
   float h[V];
-  states_of_groups<V, PART>(sh, tl, a.h0, spot, j, pl.first, a.chan, h);
+  states_of_groups<V, PART>(sh, tl, a.h0, spot, j, pl.first, a.chan, h, a.h0 && a.h0 == a.h_last);
   char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
