@@ -61,6 +61,42 @@ bool scan_strides_ok(const nvfp4_scan_args &a, int64_t sb, int64_t st) {
   return stride_ok(a.batch, sb) && stride_ok(a.time, st) && (a.time <= 1 || st >= a.chan);
 }
 
+// An output: besides, no two of its steps share memory.
+bool scan_rows_apart(const nvfp4_scan_args &a, int64_t sb, int64_t st) {
+  if (a.batch == 0 || a.time == 0) return true;
+  const int64_t b = a.batch > 1 ? sb : 0, t = a.time > 1 ? st : 0;
+  const int64_t near = b < t ? b : t, far = b < t ? t : b, n_near = b < t ? a.batch : a.time,
+                n_far = b < t ? a.time : a.batch;
+  return (n_near <= 1 || near >= a.chan) && (n_far <= 1 || far >= (n_near - 1) * near + a.chan);
+}
+
+// Whether dg and du share memory: where the ranges of addresses meet, only the same strides
+// can keep them apart (the halves of one projection's gradient).
+bool scan_grads_apart(const nvfp4_scan_args &a, const nvfp4_scan_grads &d, size_t size) {
+  if (a.batch == 0 || a.time == 0) return true;
+  const int64_t nb = a.batch - 1, nt = a.time - 1;
+  const int64_t gb = nb ? d.dg_batch : 0, gt = nt ? d.dg_time : 0, ub = nb ? d.du_batch : 0, ut = nt ? d.du_time : 0;
+  const uint64_t pg = (uint64_t)(uintptr_t)d.dg / size, pu = (uint64_t)(uintptr_t)d.du / size;
+  const uint64_t eg = (uint64_t)(nb * gb + nt * gt + a.chan), eu = (uint64_t)(nb * ub + nt * ut + a.chan);
+  if (pg <= pu ? pu - pg >= eg : pg - pu >= eu) return true;
+  if (gb != ub || gt != ut) return false;
+  // rows that lie apart: only the steps next to the distance can meet
+  const bool batch_far = gb >= gt;
+  const int64_t far = batch_far ? gb : gt, near = batch_far ? gt : gb, n_far = batch_far ? nb : nt,
+                n_near = batch_far ? nt : nb;
+  const int64_t dist = (int64_t)(pu - pg), i0 = far ? -dist / far : 0;
+  for (int64_t i = i0 - 2; i <= i0 + 2; ++i) {
+    if (i < -n_far || i > n_far) continue;
+    const int64_t v = dist + i * far, j0 = near ? -v / near : 0;
+    for (int64_t j = j0 - 2; j <= j0 + 2; ++j) {
+      if (j < -n_near || j > n_near) continue;
+      const int64_t w = v + j * near;
+      if (w > -a.chan && w < a.chan) return false;
+    }
+  }
+  return true;
+}
+
 nvfp4_status check_scan(const nvfp4_scan_args *a) {
   if (!a) return NVFP4_ERR_NULL;
   if (!scan_sizes_ok(a->batch, a->time, a->chan) || !scan_strides_ok(*a, a->g_batch, a->g_time) ||
@@ -177,6 +213,7 @@ nvfp4_status nvfp4_gated_scan_forward(const nvfp4_scan_args *a, void *workspace,
       check_workspace(workspace, workspace_bytes,
                       nvfp4_gated_scan_workspace_bytes(a->batch, a->time, a->chan, 0));
   if (ws != NVFP4_OK) return ws;
+  if (!scan_rows_apart(*a, a->y_batch, a->y_time)) return NVFP4_ERR_SHAPE;
   nvfp4::ScanLaunch s;
   memset(&s, 0, sizeof s);
   s.a = *a;
@@ -204,6 +241,9 @@ nvfp4_status nvfp4_gated_scan_backward(const nvfp4_scan_args *a, const nvfp4_sca
       check_workspace(workspace, workspace_bytes,
                       nvfp4_gated_scan_workspace_bytes(a->batch, a->time, a->chan, 1));
   if (ws != NVFP4_OK) return ws;
+  if (!scan_rows_apart(*a, d->dg_batch, d->dg_time) || !scan_rows_apart(*a, d->du_batch, d->du_time))
+    return NVFP4_ERR_SHAPE;
+  if (!scan_grads_apart(*a, *d, e)) return NVFP4_ERR_UNSUPPORTED;
   nvfp4::ScanLaunch s;
   memset(&s, 0, sizeof s);
   s.a = *a;

@@ -54,6 +54,34 @@ def ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+def apart(a, b):
+    """Whether no element of one tensor shares memory with one of the other.  Tensors whose
+    ranges of addresses meet count as sharing unless their strides are the same and rows lie
+    apart (the halves of one projection, for example), where the answer is exact."""
+    if a is None or b is None or not a.numel() or not b.numel():
+        return True
+    (a0, a1), (b0, b1) = ((t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum(
+        (n - 1) * s for n, s in zip(t.shape, t.stride())))) for t in (a, b))
+    if a1 <= b0 or b1 <= a0:
+        return True
+    dims = sorted((s, n) for n, s in zip(a.shape, a.stride()) if n > 1)
+    if (a.dtype is not b.dtype or (b0 - a0) % a.element_size() or
+            dims != sorted((s, n) for n, s in zip(b.shape, b.stride()) if n > 1)):
+        return False
+    width = 1   # of what the smaller strides span, each beyond the one before
+    for s, n in dims:
+        if s < width:
+            return False
+        width += (n - 1) * s
+
+    def meets(d, dims):   # some steps bring the distance d to zero
+        if not dims:
+            return d == 0
+        s, n = dims[-1]
+        return any(meets(d + i * s, dims[:-1]) for i in range(-d // s - 1, -d // s + 3) if abs(i) < n)
+    return not meets((b0 - a0) // a.element_size(), dims)
+
+
 def new_like(t):
     """A new contiguous tensor of t's shape and type (None for None)."""
     import torch

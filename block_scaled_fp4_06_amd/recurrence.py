@@ -20,7 +20,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 from . import nvfp4 as N
-from .launch import check, dtype_code, new_like, ptr, run_on
+from .launch import apart, check, dtype_code, new_like, ptr, run_on
 
 
 @dataclass
@@ -47,6 +47,13 @@ def _steps(name, t, shape):
     _, time, chan = shape
     if (chan > 1 and t.stride(2) != 1) or (time > 1 and t.stride(1) < chan):
         raise ValueError("%s must have unit channel stride and time steps apart" % name)
+
+
+def _output(name, t, chan):
+    """No two steps of t share memory (an expanded tensor's would)."""
+    (s0, n0), (s1, n1) = sorted(zip(_strides(t), t.shape))   # (0 for a single row or step)
+    if t.numel() and ((n0 > 1 and s0 < chan) or (n1 > 1 and s1 < (n0 - 1) * s0 + chan)):
+        raise ValueError("%s must have rows and time steps apart" % name)
 
 
 def _plain(name, t, shape, dtypes, device):
@@ -116,7 +123,7 @@ def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=No
     """The gradients of gated_scan_forward from those of y (dy) and of h_last (dh_last, None:
     zero); y as the forward call returned it.  out: (dg, du) to write into, laid out as g and
     u may be (the two halves of one projection's gradient, for example); neither may share
-    memory with an input."""
+    memory with the other or with an input."""
     import torch
     shape, dtype, dev = _check_inputs(g, u, floor, h0, reset)
     _sequence("dy", dy, shape, dtype, dev)
@@ -126,6 +133,14 @@ def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=No
     if out is not None:
         _sequence("out[0]", out[0], shape, dtype, dev)
         _sequence("out[1]", out[1], shape, dtype, dev)
+        _output("out[0]", out[0], chan)
+        _output("out[1]", out[1], chan)
+        if not apart(*out):
+            raise ValueError("out[0] and out[1] share memory")
+        for name, t in zip(("dy", "g", "u", "y", "floor", "h0", "reset", "dh_last"),
+                           (dy, g, u, y, floor, h0, reset, dh_last)):
+            if not apart(out[0], t) or not apart(out[1], t):
+                raise ValueError("out shares memory with %s" % name)
 
     def call(handle):
         dg, du = (new_like(g), new_like(g)) if out is None else out

@@ -370,7 +370,8 @@ nvfp4_status nvfp4_residual_norm_backward(const nvfp4_norm_params *p,
  * step with reset != 0, a_t = 0: h_t = u_t whatever came before (a document of a packed
  * row begins), also where what came before is inf or NaN.  y_t = h_t, rounded to the
  * tensor's type; the state itself is carried in binary32.  One step (time = 1) serves a
- * decoder.  h_last may be h0 itself; no other output shares memory with an input.  The
+ * decoder.  h_last may be h0 itself; no other output shares memory with an input, and the
+ * steps of y (and of the gradients below) lie apart.  The
  * workspace (16-byte aligned, any contents) belongs to the call until the stream has
  * passed it.  Results are the same bits every time.
  */
@@ -402,7 +403,9 @@ nvfp4_status nvfp4_gated_scan_forward(const nvfp4_scan_args *a, void *workspace,
  * nvfp4_gated_scan_backward -- with G_t = dy_t + a_{t+1} G_{t+1} (dh_last after the end):
  *   du_t = (1 - a_t) G_t,  da_t = G_t (h_{t-1} - u_t) (0 at a reset),
  *   dg_t = da_t (1 - floor) s_t (1 - s_t),  dfloor = sum da_t (1 - s_t),  dh0 = a_1 G_1.
- * h_{t-1} is read from y as it was stored.  a->h_last is not used.
+ * h_{t-1} is read from y as it was stored.  a->h_last is not used.  No output shares memory
+ * with an input or another output; dg and du may be parts of the same rows (the halves of
+ * one projection's gradient).
  */
 typedef struct {
     const void *dy;

@@ -35,3 +35,19 @@ def test_state_in_place_behind_resets(b, t, c, dtype):
             yi, s = R.gated_scan_forward(g, u, fl, state, reset, h_last=state)
             torch.cuda.synchronize()
             assert s is state and torch.equal(yi, y) and torch.equal(state, last)
+
+
+@pytest.mark.parametrize("b,t,c", [(1, 1, 8), (3, 40, 24), (2, 300, 70)])
+def test_gradients_given(b, t, c):
+    """The halves of one projection's gradient, and time-major tensors."""
+    say("scan gradients given %dx%dx%d" % (b, t, c))
+    g, u, fl, h0, reset = case(b, t, c, BF16, docs=2)
+    y, _ = R.gated_scan_forward(g, u, fl, h0, reset)
+    want = R.gated_scan_backward(u, g, u, y, fl, h0, reset)
+    both = torch.full((b, t, 2 * c + 1), 7.0, dtype=BF16, device="cuda")
+    turned = [torch.empty((t, b, c), dtype=BF16, device="cuda").transpose(0, 1) for _ in range(2)]
+    for dg, du in ((both[:, :, :c], both[:, :, c:-1]), (both[:, :, c:-1], both[:, :, :c]), turned):
+        got = R.gated_scan_backward(u, g, u, y, fl, h0, reset, out=(dg, du))
+        torch.cuda.synchronize()
+        assert got.dg is dg and torch.equal(dg, want.dg) and torch.equal(du, want.du)
+    assert bool((both[:, :, -1] == 7.0).all())
