@@ -153,7 +153,10 @@ def gated_scan_backward(dy, g, u, y, floor=None, h0=None, reset=None, dh_last=No
         check(N.nvfp4_gated_scan_backward(_args(g, u, floor, h0, reset, y, None), grads, ptr(ws),
                                           need, handle), "nvfp4_gated_scan_backward")
         return GatedScanGrads(dg, du, dh0, dfloor)
-    return run_on(stream, dev, (dy, g, u, y, floor, h0, reset, dh_last, *(out or ())), call)
+    grads = run_on(stream, dev, (dy, g, u, y, floor, h0, reset, dh_last, *(out or ())), call)
+    if out is not None:
+        torch.autograd.graph.increment_version(out)
+    return grads
 
 
 _AUTOGRAD = {}

@@ -39,7 +39,7 @@ def test_state_in_place_behind_resets(b, t, c, dtype):
 
 @pytest.mark.parametrize("b,t,c", [(1, 1, 8), (3, 40, 24), (2, 300, 70)])
 def test_gradients_given(b, t, c):
-    """The halves of one projection's gradient, and time-major tensors."""
+    """The halves of one projection's gradient, and time-major tensors: written, and marked so."""
     say("scan gradients given %dx%dx%d" % (b, t, c))
     g, u, fl, h0, reset = case(b, t, c, BF16, docs=2)
     y, _ = R.gated_scan_forward(g, u, fl, h0, reset)
@@ -47,7 +47,9 @@ def test_gradients_given(b, t, c):
     both = torch.full((b, t, 2 * c + 1), 7.0, dtype=BF16, device="cuda")
     turned = [torch.empty((t, b, c), dtype=BF16, device="cuda").transpose(0, 1) for _ in range(2)]
     for dg, du in ((both[:, :, :c], both[:, :, c:-1]), (both[:, :, c:-1], both[:, :, :c]), turned):
+        versions = dg._version, du._version
         got = R.gated_scan_backward(u, g, u, y, fl, h0, reset, out=(dg, du))
         torch.cuda.synchronize()
         assert got.dg is dg and torch.equal(dg, want.dg) and torch.equal(du, want.du)
+        assert dg._version > versions[0] and du._version > versions[1]
     assert bool((both[:, :, -1] == 7.0).all())
