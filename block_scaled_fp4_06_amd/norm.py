@@ -24,7 +24,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 from . import nvfp4 as N
-from .launch import check, dtype_code, new_like, ptr, run_on
+from .launch import apart, check, dtype_code, new_like, ptr, run_on
 
 MAX_COLS = 32768
 
@@ -130,13 +130,18 @@ def residual_norm_forward(x, z, post_weight, next_weight=None, gate=None, skip_s
     """(x_out, h, ctx): the end of one block and the beginning of the next.
 
     next_weight None: only the sum is formed and h is None.  out: where x_out goes (shape and
-    type of x; x itself for an update in place)."""
+    type of x; x itself for an update in place, and no memory of another input)."""
     import torch
     if z is None:
         raise ValueError("z is missing (norm_forward is the norm without a branch)")
     _check_operands(x, z, post_weight, next_weight, gate)
     if out is not None:
         _matrix("out", out, x.shape, x.device, x.dtype)
+        in_place = out is x or (out.data_ptr() == x.data_ptr() and out.stride() == x.stride())
+        for name, t in (("x", None if in_place else x), ("z", z), ("post_weight", post_weight),
+                        ("next_weight", next_weight), ("gate", gate)):
+            if not apart(out, t):
+                raise ValueError("out shares memory with %s" % name)
     ctx = ResidualNormContext(out, z, post_weight, next_weight, gate, None, None, skip_scale,
                               branch_scale, weight_offset)
 

@@ -291,7 +291,8 @@ typedef enum { NVFP4_DT_BF16 = 0, NVFP4_DT_FP32 = 1 } nvfp4_dtype;
  *           rstd = 1 / sqrt(mean(x_out^2) + eps) of x_out as it is stored.
  * With z NULL there is no branch: h is the norm of x itself, and x_out, rstd_post,
  * post_weight and gate are NULL.  With next_weight NULL only the sum is formed, and h and
- * rstd are NULL.  gate NULL means a gate of one.  x_out may be x itself (same row stride).
+ * rstd are NULL.  gate NULL means a gate of one.  x_out may be x itself (same row stride);
+ * otherwise no output shares memory with an input.
  */
 typedef struct {
     int64_t rows, cols;     /* cols <= NVFP4_NORM_MAX_COLS */

@@ -5,6 +5,7 @@ import os
 import pytest
 import torch
 
+from block_scaled_fp4_06_amd import norm
 from block_scaled_fp4_06_amd import nvfp4 as N
 from block_scaled_fp4_06_amd import recurrence as R
 from block_scaled_fp4_06_amd.launch import apart
@@ -81,3 +82,18 @@ def test_scan_status_of_outputs():
     for at in (0, 7, -7, 16 + 9, 80 * 2 - 9, 16 * 4 - 1):            # elements from dg
         assert sbackward(sargs(batch=3), du=2 * FAKE + 2 * at, **halves) == UNSUPPORTED, at
     assert sbackward(sargs(), dg=2 * FAKE, du=2 * FAKE + 16, du_time=16, du_batch=80) == UNSUPPORTED
+
+
+def test_norm_sum_given(no_library_calls):  # noqa: F811
+    buf, w = torch.zeros(7, 32), torch.ones(32)
+    x, z = buf[:6], torch.zeros(6, 32)
+    wide = torch.zeros(6, 64)
+    for kw, what in ((dict(out=z), "memory with z"), (dict(out=buf[1:]), "memory with x"),
+                     (dict(z=wide[:, 8:40], out=wide[:, :32]), "memory with z"),
+                     (dict(gate=wide[:1, :32], out=wide[:, :32]), "memory with gate"),
+                     (dict(post_weight=wide[2, 31:63], out=wide[:, :32]), "memory with post_weight"),
+                     (dict(z=wide[:, 32:], out=wide[:, :32]), "GPU"),
+                     (dict(x=wide[:, 32:], out=wide[:, :32]), "GPU"),
+                     (dict(out=x), "GPU"), (dict(out=buf[:6]), "GPU"), (dict(out=torch.zeros(6, 32)), "GPU")):
+        with pytest.raises(ValueError, match=what):
+            norm.residual_norm_forward(**dict(dict(x=x, z=z, post_weight=w, next_weight=w), **kw))
