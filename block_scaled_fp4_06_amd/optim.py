@@ -101,18 +101,27 @@ class AdamW:
             raise ValueError("betas must lie in [0, 1), not %r" % (betas,))
         if not eps >= 0.0:
             raise ValueError("eps must not be negative")
-        decay = weight_decay if isinstance(weight_decay, (list, tuple)) else (
-            [weight_decay] * len(self.params))
-        if len(decay) != len(self.params):
-            raise ValueError("%d weight_decay values for %d parameters" % (len(decay),
-                                                                           len(self.params)))
         self.lr, self.betas, self.eps = lr, tuple(betas), eps
-        self.weight_decay = [float(d) for d in decay]
+        self.weight_decay = weight_decay
         self.stochastic_rounding, self.seed = bool(stochastic_rounding), int(seed)
         self.state = state if state is not None else new_state(self.params, bits, master)
         self._check_state()
         self._shapes = [p.shape for p in self.params]
         self._table = None
+
+    @property
+    def weight_decay(self):
+        """One number per parameter; an assignment also takes one for all.  What a step finds
+        here is what it applies, as with lr, betas and eps."""
+        return self._weight_decay
+
+    @weight_decay.setter
+    def weight_decay(self, value):
+        decay = value if isinstance(value, (list, tuple)) else [value] * len(self.params)
+        if len(decay) != len(self.params):
+            raise ValueError("%d weight_decay values for %d parameters" % (len(decay),
+                                                                           len(self.params)))
+        self._weight_decay = [float(d) for d in decay]
 
     def _check_state(self):
         import torch
@@ -131,14 +140,16 @@ class AdamW:
 
     def _layout(self, kinds):
         """The table of tensors for gradients of these types, on the host and the device; made
-        again when a parameter's storage, the state or a gradient's type has changed."""
+        again when a parameter's storage or decay, the state or a gradient's type has changed."""
         import torch
         s = self.state
         pins = list(map(torch.Tensor.data_ptr, self.params))
         pins += [t.data_ptr() for t in (s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
                                         s.exp_avg_sq_scale, s.master) if t is not None]
-        if self._table is not None and self._table[0] == pins and self._table[1] == kinds:
-            return self._table
+        decay = self._weight_decay
+        if self._table is not None and self._table[:3] == (pins, kinds, decay):
+            return self._table[3:]
+        decay = list(decay)
         self._check_state()
         count, at = len(self.params), offsets(self.params)[0]
         rows = (N.AdamWTensor * count)()
@@ -153,14 +164,14 @@ class AdamW:
             if s.bits == 8:
                 r.exp_avg_scale = s.exp_avg_scale.data_ptr() + 4 * (a // BLOCK)
                 r.exp_avg_sq_scale = s.exp_avg_sq_scale.data_ptr() + 4 * (a // BLOCK)
-            r.weight_decay = self.weight_decay[i]
+            r.weight_decay = decay[i]
             r.param_dtype = dtype_code("params[%d]" % i, p)
             r.grad_dtype = 0 if kinds[i] == torch.bfloat16 else 1
         need = N.nvfp4_adamw_table_bytes(count)
         host = torch.empty(need, dtype=torch.uint8)
         check(N.nvfp4_adamw_table(rows, count, s.bits, host.data_ptr(), need), "nvfp4_adamw_table")
-        self._table = (pins, kinds, host, host.to(self.device))
-        return self._table
+        self._table = (pins, kinds, decay, host, host.to(self.device))
+        return self._table[3:]
 
     def _check_grads(self, grads):
         """(pointers, types) of one gradient (or None) per parameter: contiguous, of its shape,
@@ -211,7 +222,7 @@ class AdamW:
                                           s.exp_avg_scale, s.exp_avg_sq_scale, s.master)
 
         def call(handle):
-            _, _, host, device = self._layout(kinds)
+            host, device = self._layout(kinds)
             prm = N.AdamWParams(self.lr, self.betas[0], self.betas[1], self.eps, s.step + 1,
                                 self.seed, 1 if self.stochastic_rounding else 0, 0,
                                 ptr(grad_scale))
