@@ -20,8 +20,8 @@ repeat that step's values.
 """
 from __future__ import annotations
 
-from array import array
 from dataclasses import dataclass
+from struct import Struct
 from typing import Optional
 
 from . import nvfp4 as N
@@ -91,12 +91,8 @@ class AdamW:
         if not self.params:
             raise ValueError("no parameters")
         self.device = self.params[0].device
-        for i, p in enumerate(self.params):
-            dtype_code("params[%d]" % i, p)
-            if p.device != self.device:
-                raise ValueError("params[%d] is on %s, expected %s" % (i, p.device, self.device))
-            if not p.is_contiguous():
-                raise ValueError("params[%d] must be contiguous" % i)
+        self._shapes = [p.shape for p in self.params]
+        self._check_params()
         if not 0.0 <= betas[0] < 1.0 or not 0.0 <= betas[1] < 1.0:
             raise ValueError("betas must lie in [0, 1), not %r" % (betas,))
         if not eps >= 0.0:
@@ -106,7 +102,7 @@ class AdamW:
         self.stochastic_rounding, self.seed = bool(stochastic_rounding), int(seed)
         self.state = state if state is not None else new_state(self.params, bits, master)
         self._check_state()
-        self._shapes = [p.shape for p in self.params]
+        self._pack = Struct("=%dQ" % len(self.params)).pack
         self._table = None
 
     @property
@@ -122,6 +118,17 @@ class AdamW:
             raise ValueError("%d weight_decay values for %d parameters" % (len(decay),
                                                                            len(self.params)))
         self._weight_decay = [float(d) for d in decay]
+
+    def _check_params(self):
+        for i, (p, shape) in enumerate(zip(self.params, self._shapes)):
+            dtype_code("params[%d]" % i, p)
+            if p.device != self.device:
+                raise ValueError("params[%d] is on %s, expected %s" % (i, p.device, self.device))
+            if p.shape != shape:
+                raise ValueError("params[%d] has shape %s, expected %s" % (i, tuple(p.shape),
+                                                                           tuple(shape)))
+            if not p.is_contiguous():
+                raise ValueError("params[%d] must be contiguous" % i)
 
     def _check_state(self):
         import torch
@@ -143,18 +150,25 @@ class AdamW:
         again when a parameter's storage or decay, the state or a gradient's type has changed."""
         import torch
         s = self.state
-        pins = list(map(torch.Tensor.data_ptr, self.params))
-        pins += [t.data_ptr() for t in (s.exp_avg, s.exp_avg_sq, s.exp_avg_scale,
-                                        s.exp_avg_sq_scale, s.master) if t is not None]
+        each, params, table = torch.Tensor, self.params, self._table
+        used = [*params, s.exp_avg, s.exp_avg_sq]
+        if s.bits == 8:
+            used += (s.exp_avg_scale, s.exp_avg_sq_scale)
+        if s.master is not None:
+            used.append(s.master)
+        pins = list(map(each.data_ptr, used))
         decay = self._weight_decay
-        if self._table is not None and self._table[:3] == (pins, kinds, decay):
-            return self._table[3:]
+        # (a parameter may also have been given another view of the same storage)
+        if (table is not None and table[0] == pins and table[1] == kinds and table[2] == decay and
+                all(map(each.is_contiguous, params))):
+            return table
         decay = list(decay)
+        self._check_params()
         self._check_state()
-        count, at = len(self.params), offsets(self.params)[0]
+        count, at = len(params), offsets(params)[0]
         rows = (N.AdamWTensor * count)()
         width = 4 if s.bits == 32 else 1
-        for i, (p, a) in enumerate(zip(self.params, at)):
+        for i, (p, a) in enumerate(zip(params, at)):
             r = rows[i]
             r.param, r.n = ptr(p), p.numel()
             bf16 = p.dtype == torch.bfloat16
@@ -170,8 +184,9 @@ class AdamW:
         need = N.nvfp4_adamw_table_bytes(count)
         host = torch.empty(need, dtype=torch.uint8)
         check(N.nvfp4_adamw_table(rows, count, s.bits, host.data_ptr(), need), "nvfp4_adamw_table")
-        self._table = (pins, kinds, decay, host, host.to(self.device))
-        return self._table[3:]
+        device = host.to(self.device)
+        self._table = (pins, kinds, decay, host, device, host.data_ptr(), device.data_ptr())
+        return self._table
 
     def _check_grads(self, grads):
         """(pointers, types) of one gradient (or None) per parameter: contiguous, of its shape,
@@ -181,10 +196,11 @@ class AdamW:
         # all at once where all are there and right; otherwise one by one, to say which is not
         try:
             types = [g.dtype for g in grads]
-            if (all(map(each.is_contiguous, grads)) and set(types).issubset(kinds) and
+            if (all(map(each.is_contiguous, grads)) and
+                    (self._table is not None and types == self._table[1] or set(types).issubset(kinds)) and
                     list(map(each.size, grads)) == self._shapes and
-                    set(map(each.get_device, grads)) == {dev.index}):
-                return array("Q", map(each.data_ptr, grads)), types
+                    list(map(each.get_device, grads)) == [dev.index] * len(types)):
+                return self._pack(*map(each.data_ptr, grads)), types
         except (AttributeError, TypeError):
             pass
         for i, (g, shape) in enumerate(zip(grads, self._shapes)):
@@ -198,7 +214,7 @@ class AdamW:
                                  "torch.float32" % (i, g.dtype))
             if g.device != dev:
                 raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
-        return (array("Q", [0 if g is None else g.data_ptr() for g in grads]),
+        return (self._pack(*[0 if g is None else g.data_ptr() for g in grads]),
                 [p.dtype if g is None else g.dtype for g, p in zip(grads, self.params)])
 
     def step(self, grads=None, lr=None, grad_scale=None, stream=None):
@@ -212,7 +228,7 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
         dev, f32 = self.device, torch.float32
-        pointers, kinds = self._check_grads(grads)
+        pointers, kinds = self._check_grads(grads)   # (pointers: an array, as bytes)
         if grad_scale is not None:
             N._check_buffer("grad_scale", grad_scale.reshape(-1), (1,), (f32,), dev, False)
         if lr is not None:
@@ -222,15 +238,13 @@ class AdamW:
                                           s.exp_avg_scale, s.exp_avg_sq_scale, s.master)
 
         def call(handle):
-            host, device = self._layout(kinds)
+            _, _, _, _, table, host, device = self._layout(kinds)
             prm = N.AdamWParams(self.lr, self.betas[0], self.betas[1], self.eps, s.step + 1,
                                 self.seed, 1 if self.stochastic_rounding else 0, 0,
                                 ptr(grad_scale))
-            check(N.nvfp4_adamw_step(host.data_ptr(), device.data_ptr(),
-                                     pointers.buffer_info()[0], prm, handle),
-                  "nvfp4_adamw_step")
+            check(N.nvfp4_adamw_step(host, device, pointers, prm, handle), "nvfp4_adamw_step")
             if stream is not None:   # (the table may be remade before this stream has passed)
-                device.record_stream(stream)
+                table.record_stream(stream)
         run_on(stream, dev, used, call)
         torch.autograd.graph.increment_version(self.params)
         s.step += 1

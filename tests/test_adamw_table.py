@@ -26,7 +26,7 @@ class Row(ctypes.Structure):
 
 def rows(opt, kinds=None):
     """The table's rows as the optimizer would use them for a step now."""
-    table = opt._layout([p.dtype for p in opt.params] if kinds is None else kinds)[0]
+    table = opt._layout([p.dtype for p in opt.params] if kinds is None else kinds)[3]
     head = N.nvfp4_adamw_table_bytes(0)
     return [r.t for r in (Row * len(opt.params)).from_buffer_copy(table.numpy().tobytes()[head:])]
 
@@ -35,8 +35,8 @@ def test_weight_decay_between_steps():
     p = [torch.zeros(300), torch.zeros(5, 5), torch.zeros(7, dtype=BF16)]
     opt = optim.AdamW(p, weight_decay=0.1)
     assert [r.weight_decay for r in rows(opt)] == [0.1] * 3
-    table = opt._layout([F32, F32, BF16])[0]
-    assert opt._layout([F32, F32, BF16])[0] is table
+    table = opt._layout([F32, F32, BF16])
+    assert opt._layout([F32, F32, BF16]) is table
     opt.weight_decay[1] = 0.0
     assert [r.weight_decay for r in rows(opt)] == [0.1, 0.0, 0.1]
     opt.weight_decay = [0.3, 0.2, 0.1]
@@ -46,3 +46,27 @@ def test_weight_decay_between_steps():
     with pytest.raises(ValueError, match="weight_decay"):
         opt.weight_decay = [0.1]
     assert opt.weight_decay == [0.5] * 3
+
+
+def test_parameters_replaced_between_steps():
+    p = [torch.zeros(300), torch.arange(25.0).view(5, 5)]
+    opt = optim.AdamW(p)
+    old = [r.param for r in rows(opt)]
+    p[1].data = torch.ones(5, 5)
+    now = rows(opt)
+    assert now[0].param == old[0] and now[1].param == p[1].data_ptr() != old[1] and now[1].n == 25
+    p[1].data = p[1].data.to(BF16)
+    assert rows(opt)[1].param_dtype == 0
+    for data, what in ((p[1].data.t(), r"params\[1\] must be contiguous"),
+                       (torch.ones(5, 5).t(), r"params\[1\] must be contiguous"),
+                       (torch.ones(25), r"params\[1\] has shape"),
+                       (torch.ones(6, 5), r"params\[1\] has shape"),
+                       (torch.ones(5, 5).half(), r"params\[1\] has dtype")):
+        p[1].data = data
+        with pytest.raises(ValueError, match=what):
+            rows(opt)
+    p[1].data = torch.ones(5, 5)
+    assert rows(opt)[1].param == p[1].data_ptr()
+    opt.device, p[0].data = torch.device("cuda:0"), torch.zeros(300)   # moved away from its optimizer
+    with pytest.raises(ValueError, match=r"params\[0\] is on cpu"):
+        rows(opt)
