@@ -145,9 +145,10 @@ class AdamW:
         if s.master is not None:
             N._check_buffer("state.master", s.master, (end,), (torch.float32,), self.device, False)
 
-    def _layout(self, kinds):
+    def _layout(self, kinds, handle=0):
         """The table of tensors for gradients of these types, on the host and the device; made
-        again when a parameter's storage or decay, the state or a gradient's type has changed."""
+        again (on the stream of `handle`) when a parameter's storage or decay, the state or a
+        gradient's type has changed."""
         import torch
         s = self.state
         each, params, table = torch.Tensor, self.params, self._table
@@ -185,7 +186,7 @@ class AdamW:
         host = torch.empty(need, dtype=torch.uint8)
         check(N.nvfp4_adamw_table(rows, count, s.bits, host.data_ptr(), need), "nvfp4_adamw_table")
         device = host.to(self.device)
-        self._table = (pins, kinds, decay, host, device, host.data_ptr(), device.data_ptr())
+        self._table = (pins, kinds, decay, host, device, host.data_ptr(), device.data_ptr(), handle)
         return self._table
 
     def _check_grads(self, grads):
@@ -238,13 +239,13 @@ class AdamW:
                                           s.exp_avg_scale, s.exp_avg_sq_scale, s.master)
 
         def call(handle):
-            _, _, _, _, table, host, device = self._layout(kinds)
+            _, _, _, _, table, host, device, home = self._layout(kinds, handle)
             prm = N.AdamWParams(self.lr, self.betas[0], self.betas[1], self.eps, s.step + 1,
                                 self.seed, 1 if self.stochastic_rounding else 0, 0,
                                 ptr(grad_scale))
             check(N.nvfp4_adamw_step(host, device, pointers, prm, handle), "nvfp4_adamw_step")
-            if stream is not None:   # (the table may be remade before this stream has passed)
-                table.record_stream(stream)
+            if handle != home:   # (the table may be remade before this stream has passed)
+                table.record_stream(torch.cuda.current_stream(dev))
         run_on(stream, dev, used, call)
         torch.autograd.graph.increment_version(self.params)
         s.step += 1

@@ -36,3 +36,30 @@ def test_weight_decay_between_steps():
             w, m, v, _ = step32(w, host(g), m, v, t, decay[i], **HYPER)
             want[i] = w, m, v
             assert np.array_equal(host(p), w), (t, i)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_table_is_kept_for_the_stream_that_reads_it(given):
+    """The table's memory is not handed out again while a step on another stream may read it."""
+    say("adamw table on another stream, given=%s" % given)
+    params, grads = tensors([300, 5000], F32, 1), tensors([300, 5000], F32, 2)
+    opt = optim.AdamW(params, **HYPER)
+    opt.step(grads)
+    torch.cuda.synchronize()
+    old, size = opt._table[4].data_ptr(), opt._table[4].numel()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(200000000)
+        if not given:
+            opt.step(grads)
+    if given:
+        opt.step(grads, stream=other)
+    assert opt._table[4].data_ptr() == old
+    opt._table = None
+    new = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    busy = not other.query()
+    assert busy and old not in [t.data_ptr() for t in new]
+    other.synchronize()
+    opt.step(grads)
+    torch.cuda.synchronize()
+    assert opt.state.step == 3
