@@ -215,8 +215,10 @@ class AdamW:
                                  "torch.float32" % (i, g.dtype))
             if g.device != dev:
                 raise ValueError("grads[%d] is on %s, expected %s" % (i, g.device, dev))
+        # (a missing gradient has the type it had before: the table need not be made again)
+        before = self._table[1] if self._table is not None else [p.dtype for p in self.params]
         return (self._pack(*[0 if g is None else g.data_ptr() for g in grads]),
-                [p.dtype if g is None else g.dtype for g, p in zip(grads, self.params)])
+                [t if g is None else g.dtype for g, t in zip(grads, before)])
 
     def step(self, grads=None, lr=None, grad_scale=None, stream=None):
         """One update.  grads: a list like params (default: each parameter's .grad), contiguous,

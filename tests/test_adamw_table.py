@@ -70,3 +70,15 @@ def test_parameters_replaced_between_steps():
     opt.device, p[0].data = torch.device("cuda:0"), torch.zeros(300)   # moved away from its optimizer
     with pytest.raises(ValueError, match=r"params\[0\] is on cpu"):
         rows(opt)
+
+
+def test_missing_gradients_keep_the_table():
+    p = [torch.zeros(300, dtype=BF16), torch.zeros(5, 5, dtype=BF16)]
+    opt = optim.AdamW(p)
+    grads = [torch.zeros(300), torch.zeros(5, 5, dtype=BF16)]
+    table = opt._layout(opt._check_grads(grads)[1])
+    assert table[1] == [F32, BF16]
+    for missing in ((0,), (1,), (0, 1)):
+        some = [None if i in missing else g for i, g in enumerate(grads)]
+        assert opt._layout(opt._check_grads(some)[1]) is table, missing
+    assert opt._layout(opt._check_grads([None, torch.zeros(5, 5)])[1])[1] == [F32, F32]
