@@ -79,7 +79,8 @@ def new_state(params, bits=32, master=False) -> AdamWState:
 
 
 class AdamW:
-    """The optimizer of a fixed list of parameters (contiguous tensors on one GPU).
+    """The optimizer of a fixed list of parameters (contiguous tensors on one GPU, none of
+    which shares memory with another: a tied weight is listed once).
 
     weight_decay: one number, or one per parameter.  state: an AdamWState to go on with;
     by default new_state(params, bits, master).  Tensors in `state` are used, not copied."""
@@ -129,6 +130,11 @@ class AdamW:
                                                                            tuple(shape)))
             if not p.is_contiguous():
                 raise ValueError("params[%d] must be contiguous" % i)
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size(), i)
+                       for i, p in enumerate(self.params) if p.numel())
+        for (_, end, i), (begin, _, j) in zip(spans, spans[1:]):
+            if begin < end:   # (two workgroups would update the same elements)
+                raise ValueError("params[%d] and params[%d] share memory" % (min(i, j), max(i, j)))
 
     def _check_state(self):
         import torch

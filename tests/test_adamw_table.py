@@ -82,3 +82,19 @@ def test_missing_gradients_keep_the_table():
         some = [None if i in missing else g for i, g in enumerate(grads)]
         assert opt._layout(opt._check_grads(some)[1]) is table, missing
     assert opt._layout(opt._check_grads([None, torch.zeros(5, 5)])[1])[1] == [F32, F32]
+
+
+def test_parameters_that_share_memory():
+    flat = torch.zeros(40)
+    a, b = flat[:30], flat[30:]
+    optim.AdamW([b, a, torch.zeros(0), flat[:0]])
+    for params, what in (([a, torch.zeros(3), a], r"params\[0\] and params\[2\]"),
+                         ([b, flat[29:31]], r"params\[0\] and params\[1\]"),
+                         ([flat[29:31], a.view(5, 6)], r"params\[0\] and params\[1\]")):
+        with pytest.raises(ValueError, match=what + " share memory"):
+            optim.AdamW(params)
+    opt = optim.AdamW([torch.zeros(30), b])
+    rows(opt)
+    opt.params[0].data = flat[5:35]
+    with pytest.raises(ValueError, match="share memory"):
+        rows(opt)
