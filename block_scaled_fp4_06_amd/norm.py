@@ -260,6 +260,7 @@ def autograd_residual_norm():
             return x_out, h
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(fctx, dx_out, dh):
             d = residual_norm_backward(_rows_apart(dx_out), _rows_apart(dh),
                                        ResidualNormContext(*fctx.saved_tensors, *fctx.scales))
@@ -284,6 +285,7 @@ def autograd_norm():
             return h
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(fctx, dh):
             x, weight, rstd = fctx.saved_tensors
             ctx = ResidualNormContext(x, None, None, weight, None, rstd, None, 1.0, 1.0,

@@ -177,6 +177,7 @@ def autograd_gated_scan():
             return y, h_last
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(fctx, dy, dh_last):
             g, u, y, floor, h0, reset = fctx.saved_tensors
             d = gated_scan_backward(dy.contiguous(), g, u, y, floor, h0, reset,

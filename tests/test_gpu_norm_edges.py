@@ -34,3 +34,14 @@ def test_gate_gradient_of_one_row(cols, types):
         again = norm.residual_norm_backward(dx, dh, ctx)
         torch.cuda.synchronize()
         assert torch.equal(again.dgate, first.dgate) and torch.equal(again.dpost_weight, first.dpost_weight)
+
+
+def test_second_derivatives_are_refused():
+    say("norm: a gradient of a gradient raises")
+    x, z, post, nxt, gate = case(4, 64, F32, F32, F32)
+    x.requires_grad_(True)
+    for y in (norm.autograd_residual_norm().apply(x, z, post, nxt, gate, 1.0, 0.5, 1e-6, 0.0)[1],
+              norm.autograd_norm().apply(x, nxt, 1e-6, 0.0)):
+        g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g * g).sum().backward()

@@ -53,3 +53,13 @@ def test_gradients_given(b, t, c):
         assert got.dg is dg and torch.equal(dg, want.dg) and torch.equal(du, want.du)
         assert dg._version > versions[0] and du._version > versions[1]
     assert bool((both[:, :, -1] == 7.0).all())
+
+
+def test_second_derivatives_are_refused():
+    say("scan: a gradient of a gradient raises")
+    g, u, fl, h0, _ = case(2, 20, 24, F32)
+    u.requires_grad_(True)
+    y, last = R.autograd_gated_scan().apply(g, u, fl, h0, None)
+    d, = torch.autograd.grad(y.square().sum() + last.sum(), u, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (d * d).sum().backward()
