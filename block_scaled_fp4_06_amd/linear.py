@@ -81,6 +81,7 @@ def autograd_linear():
             return y
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(fctx, dy):
             dx, dw = linear_backward(dy.contiguous(), fctx.lin, dw_dtype=torch.bfloat16)
             return dx, dw, None, None
