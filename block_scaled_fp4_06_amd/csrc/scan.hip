@@ -134,13 +134,11 @@ __device__ __forceinline__ void sigmoids(float g, float &s, float &sc) {
   sc = g < 0.0f ? 1.0f - s : e * s;
 }
 
-// The decay a = floor + (1 - floor) sigmoid(g) and 1 - a, in fewer instructions: the
-// exponential stops at 2^125, so sigmoid(g) ends at 2^-125 instead of zero, which adds
-// nothing to a sum with (1 - a) u.  (minimum, unlike min, lets a NaN through.)
+// The decay a = floor + (1 - floor) sigmoid(g) and 1 - a.
 template <bool FLOOR>
 __device__ __forceinline__ void decay(float g, float fl, float &a, float &w) {
-  const float e = __builtin_elementwise_minimum(__expf(-g), 0x1p125f);
-  const float s = __builtin_amdgcn_rcpf(1.0f + e), sc = e * s;
+  float s, sc;
+  sigmoids(g, s, sc);
   a = FLOOR ? __builtin_fmaf(1.0f - fl, s, fl) : s;
   w = FLOOR ? (1.0f - fl) * sc : sc;
 }

@@ -63,3 +63,28 @@ def test_second_derivatives_are_refused():
     d, = torch.autograd.grad(y.square().sum() + last.sum(), u, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (d * d).sum().backward()
+
+
+@pytest.mark.parametrize("t", [16, 17, 128, 300])
+@pytest.mark.parametrize("floor", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_closed_gate_behind_large_states(t, floor, dtype):
+    """A gate of -inf gives a = floor exactly, whatever the number of steps."""
+    say("scan: gate of -inf behind large states, t=%d floor=%s %s" % (t, floor, dtype))
+    c = 70
+    g = torch.full((1, t, c), float("inf"), dtype=dtype, device="cuda")   # steps left out
+    u = torch.zeros((1, t, c), dtype=dtype, device="cuda")
+    fl = torch.linspace(0.0, 0.75, c, device="cuda") if floor else None
+    h0 = torch.full((1, c), 3e38, device="cuda")
+    h0[0, ::3] = -3e38
+    g[0, t // 2] = float("-inf")
+    y, last = R.gated_scan_forward(g, u, fl, h0)
+    torch.cuda.synchronize()
+    want = h0 * fl if floor else torch.zeros_like(h0)
+    assert torch.equal(last, want) and torch.equal(y[:, -1], want.to(dtype))
+    assert torch.equal(y[:, t // 2 - 1], h0.to(dtype))
+    h0[:] = float("inf")   # zero times inf, as by the formula
+    y, last = R.gated_scan_forward(g, u, fl, h0)
+    torch.cuda.synchronize()
+    closed = torch.ones(c, dtype=torch.bool, device="cuda") if fl is None else fl == 0
+    assert bool(last[0, closed].isnan().all()) and bool((last[0, ~closed] == float("inf")).all())
