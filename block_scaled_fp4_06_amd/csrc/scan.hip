@@ -126,19 +126,36 @@ __device__ __forceinline__ void load_f32(const float *p, int64_t i, int cnt, flo
 }
 
 // ---------------------------------------------------------------- arithmetic
+// exp(-g).  A product with log2(e) in 24 bits is off by up to |g| 2^-25 before the
+// exponential, which bf16 results do not notice (|g| up to 2^15 still leaves their rounding the
+// larger error where the result is not zero).  binary32 gets the product's error back as a
+// factor: for |g| of 20 to 40 sigmoid(-g) is off by 3.6e-8 (rms), 8.4e-7 without.  (Clamped
+// to where it is zero, and to log(2^128), where it is infinite: both products stay finite and
+// the factor of the infinite one positive.)
+template <bool F32>
+__device__ __forceinline__ float exp_minus(float g) {
+  if constexpr (!F32) return __expf(-g);
+  constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(-g, 0x1.62e43p+6f), -150.0f);
+  const float t = x * kLog2e, r = __builtin_fmaf(x, kRest, __builtin_fmaf(x, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * kLn2, e);
+}
+
 // sigmoid(g) and sigmoid(-g), neither by a difference of near equals: for g < 0, where
 // exp(-g) may overflow (then sigmoid(g) is zero), 1 - sigmoid(g) loses nothing.
+template <bool F32>
 __device__ __forceinline__ void sigmoids(float g, float &s, float &sc) {
-  const float e = __expf(-g);
+  const float e = exp_minus<F32>(g);
   s = __builtin_amdgcn_rcpf(1.0f + e);
   sc = g < 0.0f ? 1.0f - s : e * s;
 }
 
 // The decay a = floor + (1 - floor) sigmoid(g) and 1 - a.
-template <bool FLOOR>
+template <bool F32, bool FLOOR>
 __device__ __forceinline__ void decay(float g, float fl, float &a, float &w) {
   float s, sc;
-  sigmoids(g, s, sc);
+  sigmoids<F32>(g, s, sc);
   a = FLOOR ? __builtin_fmaf(1.0f - fl, s, fl) : s;
   w = FLOOR ? (1.0f - fl) * sc : sc;
 }
@@ -469,7 +486,7 @@ __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Til
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float w;
-      decay<FLOOR>(g[s].get(i), fl[i], av[s][i], w);
+      decay<F32, FLOOR>(g[s].get(i), fl[i], av[s][i], w);
       bv[s][i] = w * u[s].get(i);
       p[i] = Pair{av[s][i] * p[i].a, __builtin_fmaf(av[s][i], p[i].b, bv[s][i])};
     }
@@ -552,7 +569,7 @@ __global__ __launch_bounds__(64) void scan_forward_short_kernel(nvfp4_scan_args 
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         float s, sc;
-        sigmoids(g.get(k), s, sc);
+        sigmoids<F32>(g.get(k), s, sc);
         const float rest = 1.0f - fl[k], x = __builtin_fmaf(rest, s, fl[k]);
         h[k] = cut ? u.get(k) : __builtin_fmaf(x, h[k], rest * sc * u.get(k));
       }
@@ -577,7 +594,7 @@ __device__ __forceinline__ void backward_step(const Raw<F32> &g, const Raw<F32> 
 #pragma unroll
   for (int i = 0; i < Raw<F32>::V; ++i) {
     float s, sc;
-    sigmoids(g.get(i), s, sc);
+    sigmoids<F32>(g.get(i), s, sc);
     const float rest = 1.0f - fl[i], grad = dy.get(i) + c[i], w = FLOOR ? rest * sc : sc;
     float da = grad * (before[i] - u.get(i));
     du[i] = w * grad;
@@ -669,7 +686,7 @@ __device__ __forceinline__ void backward_tile(const ScanLaunch &l, const Tiling 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float x, w;
-      decay<FLOOR>(g[s].get(i), fl[i], x, w);
+      decay<F32, FLOOR>(g[s].get(i), fl[i], x, w);
       p[i] = Pair{x * p[i].a, x * (p[i].b + dy[s].get(i))};
     }
     if (RESET && __any(cut[s])) {   // (one branch for the wave: resets are few)

@@ -88,3 +88,38 @@ def test_closed_gate_behind_large_states(t, floor, dtype):
     torch.cuda.synchronize()
     closed = torch.ones(c, dtype=torch.bool, device="cuda") if fl is None else fl == 0
     assert bool(last[0, closed].isnan().all()) and bool((last[0, ~closed] == float("inf")).all())
+
+
+@pytest.mark.parametrize("t", [1, 16, 200])
+def test_float32_gates_of_any_size(t):
+    """1 - a of float32 gates to a few roundings, however large they are: y = (1 - a) u from a
+    state of zero at every reset-free first step, here one step per sequence or a reset state.
+
+    Bound (u = 2^-24): exponential 2 u (product's tail, function, factor), 1 + e half, quotient
+    2 u, product 1 u: 6 u, twice that with the state's own rounding."""
+    say("scan: float32 gates of any size, t=%d" % t)
+    c = 4096
+    g = torch.zeros((1, t, c), device="cuda")
+    g[0, t // 2] = torch.linspace(-86.0, 86.0, c)
+    u = torch.zeros((1, t, c), device="cuda")
+    u[0, t // 2] = 1.0
+    y, _ = R.gated_scan_forward(g, u)
+    torch.cuda.synchronize()
+    want = 1.0 / (1.0 + torch.exp(g[0, t // 2].double()))
+    off = ((y[0, t // 2].double() - want) / want).abs()
+    assert float(off.max()) <= 12 * 2.0 ** -24, float(off.max())
+    # and a itself, behind a state of one
+    g[0], u[0] = float("inf"), 0.0
+    g[0, t // 2] = torch.linspace(-86.0, 86.0, c)
+    y, last = R.gated_scan_forward(g, u, None, torch.ones((1, c), device="cuda"))
+    torch.cuda.synchronize()
+    want = 1.0 / (1.0 + torch.exp(-g[0, t // 2].double()))
+    off = ((last[0].double() - want) / want).abs()
+    assert float(off.max()) <= 12 * 2.0 ** -24, float(off.max())
+    d = R.gated_scan_backward(torch.ones_like(y), g, u, y, None, torch.ones((1, c), device="cuda"))
+    torch.cuda.synchronize()
+    # the gate's step: G = steps from it to the end, du = (1 - a) G
+    grad = float(t - t // 2)
+    want = grad / (1.0 + torch.exp(g[0, t // 2].double()))
+    off = ((d.du[0, t // 2].double() - want) / want).abs()
+    assert float(off.max()) <= 12 * 2.0 ** -24, float(off.max())
