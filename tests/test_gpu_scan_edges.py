@@ -6,7 +6,7 @@ torch = pytest.importorskip("torch")
 
 from block_scaled_fp4_06_amd import nvfp4 as N  # noqa: E402
 from block_scaled_fp4_06_amd import recurrence as R  # noqa: E402
-from test_gpu_scan import BF16, F32, case, say  # noqa: E402
+from test_gpu_scan import BF16, F32, case, check_backward, check_forward, rnd, say  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,33 @@ def test_float32_gates_of_any_size(t):
     want = grad / (1.0 + torch.exp(g[0, t // 2].double()))
     off = ((d.du[0, t // 2].double() - want) / want).abs()
     assert float(off.max()) <= 12 * 2.0 ** -24, float(off.max())
+
+
+@pytest.mark.parametrize("b,t,c", [(1, 300, 960), (3, 520, 640), (1, 140, 1000), (31, 17, 64)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_strips_shared_unevenly(b, t, c, dtype):
+    """Strips a little fewer than a multiple of eight: some dies have one strip less, and their
+    workgroups at its place have none."""
+    say("scan strips shared unevenly %dx%dx%d %s" % (b, t, c, dtype))
+    g, u, fl, h0, reset = case(b, t, c, dtype, docs=2, seed=c)
+    y, _ = check_forward(g, u, fl, h0, reset)
+    check_backward(rnd((b, t, c), dtype, 8), g, u, y, fl, h0, reset, rnd((b, c), F32, 9))
+
+
+def test_more_strips_and_tiles_than_one_launch_takes():
+    say("scan of more strips and tiles than one launch takes")
+    b, t, c = (1 << 20) + 9, 1100, 1   # 9 tiles a strip: launches of 8, twice
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    g, u = (torch.randn(b, t, c, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    h0 = torch.randn(b, c, generator=gen, device="cuda")
+    y, last = R.gated_scan_forward(g, u, None, h0)
+    d = R.gated_scan_backward(u, g, u, y, None, h0, None, h0)
+    torch.cuda.synchronize()
+    for first, end in ((0, 5), ((1 << 20) - 3, b), (777777, 777790)):
+        rows = slice(first, end)
+        y1, last1 = R.gated_scan_forward(g[rows], u[rows], None, h0[rows])
+        d1 = R.gated_scan_backward(u[rows], g[rows], u[rows], y1, None, h0[rows], None, h0[rows])
+        torch.cuda.synchronize()
+        assert torch.equal(y[rows], y1) and torch.equal(last[rows], last1)
+        for name in ("dg", "du", "dh0"):
+            assert torch.equal(getattr(d, name)[rows], getattr(d1, name)), name
