@@ -45,3 +45,44 @@ def test_second_derivatives_are_refused():
         g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (g * g).sum().backward()
+
+
+@pytest.mark.parametrize("cols", [5121, 6000, 8192, 8193, 9001, 10240, 16384, 16385, 20481])
+@pytest.mark.parametrize("rows,gates", [(1, 1), (9, 3), (300, 1), (300, 6), (260, 260)])
+def test_wide_rows(rows, gates, cols):
+    """Widths at both ends of every form of the kernels, and the gate rows between slots."""
+    say("norm wide rows %dx%d, %d gate rows" % (rows, cols, gates))
+    for xt, zt, wt in ((BF16, BF16, F32), (F32, BF16, BF16), (F32, F32, F32)):
+        x, z, post, nxt, gate = case(rows, cols, xt, zt, wt, gates, seed=cols + rows)
+        ctx = check_forward(x, z, post, nxt, gate, skip=0.9, branch=0.5)
+        dx, dh = rnd((rows, cols), xt, 9), rnd((rows, cols), zt, 10)
+        d = check_backward(ctx, dx, dh)
+        again = norm.residual_norm_backward(dx, dh, ctx)
+        torch.cuda.synchronize()
+        for name in ("dx", "dz", "dpost_weight", "dnext_weight", "dgate"):
+            assert torch.equal(getattr(d, name), getattr(again, name)), name
+
+
+@pytest.mark.parametrize("cols", [7, 72, 513, 2048, 5120, 6001, 9001])
+def test_backward_in_place(cols):
+    """dx in dx_out's place and dz in dh's, as the C entry point allows."""
+    say("norm backward in place, %d cols" % cols)
+    rows = 37
+    x, z, post, nxt, gate = case(rows, cols)
+    _, _, ctx = norm.residual_norm_forward(x, z, post, nxt, gate)
+    dx, dh = rnd((rows, cols), BF16, 9), rnd((rows, cols), BF16, 10)
+    want = norm.residual_norm_backward(dx, dh, ctx)
+    prm = N.NormParams(rows, cols, 1, 0, 0, 1, 1 if gate.dtype == F32 else 0, 0.0, 0.0, 1.0, 1.0)
+    sums = [torch.empty(cols, device="cuda") for _ in range(2)]
+    dgate = torch.empty_like(gate)
+    need = N.nvfp4_residual_norm_workspace_bytes(prm)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    p = [t.data_ptr() for t in (ctx.x_out, z, post, gate, nxt, ctx.rstd, ctx.rstd_post, dx, dh, *sums, dgate)]
+    args = N.NormBackwardArgs(p[0], cols, p[1], cols, p[2], p[3], cols, p[4], p[5], p[6], p[7], cols, p[8],
+                              cols, p[7], cols, p[8], cols, p[9], p[10], p[11], cols)
+    assert N.nvfp4_residual_norm_backward(prm, args, ws.data_ptr(), need,
+                                          torch.cuda.current_stream().cuda_stream) == N.NVFP4_OK
+    torch.cuda.synchronize()
+    for got, w in ((dx, want.dx), (dh, want.dz), (sums[0], want.dpost_weight),
+                   (sums[1], want.dnext_weight), (dgate, want.dgate)):
+        assert torch.equal(got, w)
