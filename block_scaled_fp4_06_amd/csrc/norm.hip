@@ -28,7 +28,7 @@
 //    strips of columns that walk down the rows.
 //
 // Measured at 8192 x 5120 (bf16, fp32 weights, one gate row): forward 66 us, 5.1 TB/s, the
-// rate of a copy; backward 114 us, 4.4 TB/s, of which the sums over rows take 5.
+// rate of a copy; backward 115 us, 4.4 TB/s, of which the sums over rows take 5.
 // 2048 x 20480, two passes backward: 88 and 205 us.  One row of 5120: 4 us.
 #include "norm_rows.hpp"
 #include "nvfp4_device.hpp"
@@ -491,22 +491,36 @@ __device__ __forceinline__ void finish_row(const NormBackward &b, int64_t row, c
   if (b.a.z) store<ZF>(b.a.dz, row * b.a.ld_dz + at.col, at.cnt, dz, at.own);
 }
 
-// Walks over `count` rows from `row` on, the next row's operands in flight, and the groups'
-// ends between them.  (The streams of a workgroup take the same number of turns: do_row gets
-// the row's index, whether it is before `end`, and its operands.)
-template <bool PART, bool XF, bool ZF, class Row>
+// Walks over `count` rows from `row` on, R at a time (do_rows: the first one's index, which
+// of them are before `end`, their operands; the streams of a workgroup take the same number
+// of turns), the next R rows' operands in flight, and the groups' ends between them.  ONE:
+// all rows are of one group, so nothing but s is kept for dpost and dgate along the way;
+// otherwise R is 1.
+template <int R, bool ONE, bool PART, bool XF, bool ZF, class Rows>
 __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp, int64_t row, int64_t end,
-                                          int64_t count, const Place<PART> &at, Columns &c, Row &&do_row) {
+                                          int64_t count, const Place<PART> &at, Columns &c, Rows &&do_rows) {
+  static_assert(ONE || R == 1, "groups may end after any row");
   const int64_t per = sp.rows / sp.groups, last = max((int64_t)0, min(end, sp.rows) - 1);
   int64_t group = min(row, last) / per, left = (group + 1) * per - row;   // rows of the group from here on
+  const bool closes = closes_group(row, end);
   open_slot(b, group, at, c);
-  Operands<XF, ZF> o, ahead;
-  fetch_row<PART>(b.a, min(row, last), at, ahead);
-  for (int64_t i = 0; i < count; ++i, ++row) {
-    o = ahead;
-    if (i + 1 < count) fetch_row<PART>(b.a, min(row + 1, last), at, ahead);
-    do_row(min(row, last), row < end, o);
-    if (closes_group(row, end, left--)) {
+  Operands<XF, ZF> o[R], ahead[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) fetch_row<PART>(b.a, min(row + k, last), at, ahead[k]);
+  for (int64_t i = 0; i < count; i += R, row += R) {
+    int64_t rows[R];
+    bool live[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      o[k] = ahead[k];
+      rows[k] = min(row + k, last);
+      live[k] = row + k < end;
+    }
+    if (i + R < count)
+#pragma unroll
+      for (int k = 0; k < R; ++k) fetch_row<PART>(b.a, min(row + R + k, last), at, ahead[k]);
+    do_rows(rows, live, o);
+    if (!ONE && row < end && (--left == 0 || row + 1 == end)) {
       close_group(b, sp, group, at, c);
       if (row + 1 < end) {
         open_group(b, ++group, at, c);
@@ -514,6 +528,7 @@ __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp
       }
     }
   }
+  if (ONE && closes) close_group(b, sp, group, at, c);
 }
 
 // The sums of a workgroup's streams, added in order through LDS, into the workspace.  (A
@@ -541,15 +556,15 @@ __device__ __forceinline__ void close_slots(const NormBackward &b, const Split &
   }
 }
 
-// blockDim = (64 waves, streams).  THREADS bounds the workgroup: fewer threads leave more
-// registers to each (8192 x 5120 in binary32, ten waves: 211 us, 218 with 1024's bounds; in
-// bf16 114 either way).
+// blockDim = (64 waves, streams): R rows per stream at a time, whose sums share one
+// reduction.  THREADS bounds the workgroup: fewer threads leave more registers to each.
 // What keeps it from a copy's rate is a row's way through the reduction with one workgroup
-// to a CU: rstd fetched ahead with its row took 16384 x 2560 from 127 to 110 us; two rows to
-// a reduction take 115 at 8192 x 5120, and registers for a second workgroup spill (247).
-template <bool XF, bool ZF, int THREADS, bool PART>
+// to a CU; two rows at a time took 8192 x 5120 from 131 to 121 us, rstd fetched
+// ahead with its row from 119 to 115 (16384 x 2560 from 127 to 110), and registers for a
+// second workgroup spill (247 us).
+template <bool XF, bool ZF, int THREADS, int R, bool ONE, bool PART>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, Split sp) {
-  __shared__ float part[2][16][3];
+  __shared__ float part[2][16][3 * R];
   extern __shared__ float lds[];
   const int cols = (int)b.p.cols, waves = blockDim.x >> 6, streams = blockDim.y;
   const int64_t slot = (int64_t)blockIdx.x * streams + wave_y();
@@ -566,13 +581,25 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, 
       count = max(count, r1 - r0);
     }
   Columns c;
-  walk_rows<PART, XF, ZF>(b, sp, row, end, count, at, c, [&](int64_t i, bool live, Operands<XF, ZF> &o) {
-    float s[3] = {0.0f, 0.0f, 0.0f}, m1, m2;
-    partial_sums(o, c, s);
-    row_sum<3>(s, part, turn, waves);
-    means_of(s, o.r, o.rp, scale, m1, m2);
-    o.unpack_again();
-    if (live) finish_row(b, i, o, at, m1, m2, c);
+  walk_rows<R, ONE, PART, XF, ZF>(b, sp, row, end, count, at, c,
+                                  [&](const int64_t (&rows)[R], const bool (&live)[R], Operands<XF, ZF> (&o)[R]) {
+    float s[3 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float t[3] = {0.0f, 0.0f, 0.0f};
+      partial_sums(o[k], c, t);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) s[3 * k + i] = t[i];
+    }
+    row_sum<3 * R>(s, part, turn, waves);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float t[3] = {s[3 * k], s[3 * k + 1], s[3 * k + 2]};
+      float m1, m2;
+      means_of(t, o[k].r, o[k].rp, scale, m1, m2);
+      o[k].unpack_again();
+      if (live[k]) finish_row(b, rows[k], o[k], at, m1, m2, c);
+    }
   });
   close_slots(b, sp, blockIdx.x, at, c, lds);
 }
@@ -612,8 +639,10 @@ __global__ __launch_bounds__(256) void norm_strips_kernel(NormBackward b, Split 
   int64_t row, end;
   slot_rows(sp, slot, row, end);
   Columns c;
-  walk_rows<false, XF, ZF>(b, sp, row, end, end - row, at, c, [&](int64_t i, bool, Operands<XF, ZF> &o) {
-    finish_row(b, i, o, at, means[2 * i], means[2 * i + 1], c);
+  walk_rows<1, false, false, XF, ZF>(b, sp, row, end, end - row, at, c,
+                                     [&](const int64_t (&rows)[1], const bool (&)[1], Operands<XF, ZF> (&o)[1]) {
+    const int64_t i = rows[0];
+    finish_row(b, i, o[0], at, means[2 * i], means[2 * i + 1], c);
   });
   close_slots(b, sp, slot, at, c, nullptr);   // (one stream)
 }
@@ -699,9 +728,7 @@ hipError_t run_forward(const NormForward &n, hipStream_t stream) {
 
 template <bool XF, bool ZF>
 hipError_t forward_of(const NormForward &n, hipStream_t stream) {
-  // as few elements per thread as the workgroup's threads allow; up to 20480 columns, ten
-  // waves' bounds, which leave more registers to each thread (2048 rows of 16400 columns 74
-  // us, of 20480 90 us, with 1024 threads' bounds 88 and 104)
+  // as few elements per thread as the workgroup's threads allow
   const int64_t cols = n.p.cols;
   if (cols < 8) return run_forward<XF, ZF, 1, true, 1024, true>(n, stream);
   if (cols <= 8192) return run_forward<XF, ZF, 1, true, 1024>(n, stream);
@@ -717,9 +744,11 @@ hipError_t backward_of(const NormBackward &b, const Split &sp, hipStream_t strea
     const dim3 block(64 * waves, sp.streams);
     const size_t lds = (size_t)(sp.streams - 1) * 8 * block.x * sizeof(float);
     const uint32_t grid = (uint32_t)sp.sums;
-    if (b.p.cols < 8) norm_backward_kernel<XF, ZF, 640, true><<<grid, block, lds, stream>>>(b, sp);
-    else if (waves > 10) norm_backward_kernel<XF, ZF, 1024, false><<<grid, block, lds, stream>>>(b, sp);
-    else norm_backward_kernel<XF, ZF, 640, false><<<grid, block, lds, stream>>>(b, sp);
+    const bool one = sp.parts > 0 || sp.groups == 1;
+    if (b.p.cols < 8) norm_backward_kernel<XF, ZF, 640, 1, false, true><<<grid, block, lds, stream>>>(b, sp);
+    else if (waves > 10) norm_backward_kernel<XF, ZF, 1024, 1, false, false><<<grid, block, lds, stream>>>(b, sp);
+    else if (one) norm_backward_kernel<XF, ZF, 640, XF || ZF ? 1 : 2, true, false><<<grid, block, lds, stream>>>(b, sp);
+    else norm_backward_kernel<XF, ZF, 640, 1, false, false><<<grid, block, lds, stream>>>(b, sp);
     return hipGetLastError();
   }
   float *means = static_cast<float *>(b.ws) + 3 * sp.sums * b.p.cols;

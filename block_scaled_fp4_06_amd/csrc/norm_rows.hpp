@@ -51,11 +51,9 @@ __host__ __device__ inline void slot_rows(const Split &s, int64_t slot, int64_t 
   }
 }
 
-// Whether a slot that ends before row `end` ends a group with `row`, `left` rows of which
-// there were from it on.  (A slot without rows ends none: where one row is all there is, its
-// sums, zero, must not go where the row's slot writes the gate's gradient.)
-__host__ __device__ inline bool closes_group(int64_t row, int64_t end, int64_t left) {
-  return row < end && (left == 1 || row + 1 == end);
-}
+// Whether a slot of the rows r0 .. r1 - 1 ends a group at its last row.  An empty slot does
+// not: where one row is all there is, a workgroup has slots without rows, whose sums (zero)
+// must not go where the row's slot writes the gate's gradient.
+__host__ __device__ inline bool closes_group(int64_t r0, int64_t r1) { return r0 < r1; }
 
 }  // namespace nvfp4

@@ -17,16 +17,16 @@ static bool check(int64_t rows, int64_t groups, int streams, int64_t workgroups)
   for (int64_t slot = 0; slot < s.sums * streams; ++slot) {   // (the last ones may have no rows)
     int64_t row, end;
     slot_rows(s, slot, row, end);
+    const int64_t last = (end < rows ? end : rows) - 1 > 0 ? (end < rows ? end : rows) - 1 : 0;
+    const int64_t group = (row < last ? row : last) / per;
     for (int64_t r = row; r < end; ++r) ++rows_seen[r];
-    if (s.parts) good &= row >= end || row / per == (end - 1) / per;   // (a slot stays in one group)
-    // as the kernel walks, some turns past its rows
-    int64_t group = (row < end ? row : rows - 1) / per, left = (group + 1) * per - row;
-    for (int64_t r = row; r < end + 3; ++r)
-      if (closes_group(r, end, left--)) {
-        good &= group == r / per;
-        ++gates_written[group++];
-        left = per;
-      }
+    if (s.parts) {   // sums through the workspace: a slot stays in one group
+      good &= row >= end || row / per == (end - 1) / per;
+    } else if (groups == 1) {   // the kernel that keeps one group's sums closes it at its end
+      if (closes_group(row, end)) ++gates_written[group];
+    } else {   // a group is closed at its last row
+      for (int64_t r = row; r < end; ++r) gates_written[r / per] += (r + 1) % per == 0 || r + 1 == end;
+    }
   }
   for (int n : rows_seen) good &= n == 1;
   if (s.parts == 0)
