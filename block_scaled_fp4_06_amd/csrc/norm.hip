@@ -27,9 +27,9 @@
 //  * Rows too long for that (over kMaxRow columns) take two passes: the row sums first, then
 //    strips of columns that walk down the rows.
 //
-// Measured at 8192 x 5120 (bf16, fp32 weights, one gate row): forward 66 us, 5.1 TB/s, the
-// rate of a copy; backward 115 us, 4.4 TB/s, of which the sums over rows take 5.
-// 2048 x 20480, two passes backward: 88 and 205 us.  One row of 5120: 4 us.
+// Measured at 8192 x 5120 (bf16, fp32 weights, one gate row): forward 67 us, 5.0 TB/s (a
+// copy reaches 5.4); backward 115 us, 4.4 TB/s, of which the sums over rows take 5.
+// 2048 x 20480, two passes backward: 90 and 211 us.  One row of 5120: 4 us.
 #include "norm_rows.hpp"
 #include "nvfp4_device.hpp"
 #include "train_launch.hpp"
@@ -216,7 +216,7 @@ __device__ __forceinline__ void fetch(const void *p, int64_t i, int cnt, Raw<F32
 
 // ---------------------------------------------------------------- forward
 // blockDim = (64 waves, rows at a time); rows at a time is 1 unless waves is 1.  A row in
-// registers is read once: 66 us at 8192 x 5120, where a second reading from the caches took
+// registers is read once: 67 us at 8192 x 5120, where a second reading from the caches took
 // 265.  HOLD: the
 // weights (and a gate shared by all rows) stay in registers and the next row is fetched
 // ahead; rows of more than 16384 columns leave no registers for either.  THREADS bounds the
@@ -502,7 +502,6 @@ __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp
   static_assert(ONE || R == 1, "groups may end after any row");
   const int64_t per = sp.rows / sp.groups, last = max((int64_t)0, min(end, sp.rows) - 1);
   int64_t group = min(row, last) / per, left = (group + 1) * per - row;   // rows of the group from here on
-  const bool closes = closes_group(row, end);
   open_slot(b, group, at, c);
   Operands<XF, ZF> o[R], ahead[R];
 #pragma unroll
@@ -528,7 +527,7 @@ __device__ __forceinline__ void walk_rows(const NormBackward &b, const Split &sp
       }
     }
   }
-  if (ONE && closes) close_group(b, sp, group, at, c);
+  if (ONE) close_group(b, sp, group, at, c);
 }
 
 // The sums of a workgroup's streams, added in order through LDS, into the workspace.  (A
@@ -557,11 +556,14 @@ __device__ __forceinline__ void close_slots(const NormBackward &b, const Split &
 }
 
 // blockDim = (64 waves, streams): R rows per stream at a time, whose sums share one
-// reduction.  THREADS bounds the workgroup: fewer threads leave more registers to each.
+// reduction.  THREADS bounds the workgroup: fewer threads leave more registers to each (8192 x
+// 5120 in binary32, ten waves: 211 us, 218 with 1024's bounds).
 // What keeps it from a copy's rate is a row's way through the reduction with one workgroup
-// to a CU; two rows at a time took 8192 x 5120 from 131 to 121 us, rstd fetched
-// ahead with its row from 119 to 115 (16384 x 2560 from 127 to 110), and registers for a
-// second workgroup spill (247 us).
+// to a CU; rstd fetched ahead with its row took 8192 x 5120 from 119 to 115 us (16384 x 2560
+// from 127 to 110), and registers for a second workgroup spill (247 us).  Two rows at a time
+// (one): 8192 x 2560 55 us (57), 16384 x 2560 110.5 (113), 65536 x 256 53.3 (54.3), but 8192 x
+// 5120 115.3 (113.5), 16384 x 2048 90.9 (89.5); with 1024 threads they spill, 8192 x 6144 136
+// us (287).
 template <bool XF, bool ZF, int THREADS, int R, bool ONE, bool PART>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackward b, Split sp) {
   __shared__ float part[2][16][3 * R];
@@ -728,7 +730,9 @@ hipError_t run_forward(const NormForward &n, hipStream_t stream) {
 
 template <bool XF, bool ZF>
 hipError_t forward_of(const NormForward &n, hipStream_t stream) {
-  // as few elements per thread as the workgroup's threads allow
+  // as few elements per thread as the workgroup's threads allow; up to 20480 columns, ten
+  // waves' bounds, which leave more registers to each thread (2048 rows of 16400 columns 74
+  // us, of 20480 90 us, with 1024 threads' bounds 88 and 104)
   const int64_t cols = n.p.cols;
   if (cols < 8) return run_forward<XF, ZF, 1, true, 1024, true>(n, stream);
   if (cols <= 8192) return run_forward<XF, ZF, 1, true, 1024>(n, stream);
@@ -744,7 +748,7 @@ hipError_t backward_of(const NormBackward &b, const Split &sp, hipStream_t strea
     const dim3 block(64 * waves, sp.streams);
     const size_t lds = (size_t)(sp.streams - 1) * 8 * block.x * sizeof(float);
     const uint32_t grid = (uint32_t)sp.sums;
-    const bool one = sp.parts > 0 || sp.groups == 1;
+    const bool one = one_group(sp);
     if (b.p.cols < 8) norm_backward_kernel<XF, ZF, 640, 1, false, true><<<grid, block, lds, stream>>>(b, sp);
     else if (waves > 10) norm_backward_kernel<XF, ZF, 1024, 1, false, false><<<grid, block, lds, stream>>>(b, sp);
     else if (one) norm_backward_kernel<XF, ZF, 640, XF || ZF ? 1 : 2, true, false><<<grid, block, lds, stream>>>(b, sp);

@@ -51,9 +51,10 @@ __host__ __device__ inline void slot_rows(const Split &s, int64_t slot, int64_t 
   }
 }
 
-// Whether a slot of the rows r0 .. r1 - 1 ends a group at its last row.  An empty slot does
-// not: where one row is all there is, a workgroup has slots without rows, whose sums (zero)
-// must not go where the row's slot writes the gate's gradient.
-__host__ __device__ inline bool closes_group(int64_t r0, int64_t r1) { return r0 < r1; }
+// Whether the form of the kernel that closes one group per slot, whether or not the slot has
+// rows, may be taken: where groups are in parts, whose sums all go through the workspace.
+// Slots of whole groups write the gate's gradient themselves, and where one row is all there is,
+// its workgroup also has slots without rows, which must not write (zero) in its place.
+__host__ __device__ inline bool one_group(const Split &s) { return s.parts > 0; }
 
 }  // namespace nvfp4

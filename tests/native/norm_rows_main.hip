@@ -20,10 +20,9 @@ static bool check(int64_t rows, int64_t groups, int streams, int64_t workgroups)
     const int64_t last = (end < rows ? end : rows) - 1 > 0 ? (end < rows ? end : rows) - 1 : 0;
     const int64_t group = (row < last ? row : last) / per;
     for (int64_t r = row; r < end; ++r) ++rows_seen[r];
-    if (s.parts) {   // sums through the workspace: a slot stays in one group
-      good &= row >= end || row / per == (end - 1) / per;
-    } else if (groups == 1) {   // the kernel that keeps one group's sums closes it at its end
-      if (closes_group(row, end)) ++gates_written[group];
+    if (s.parts) good &= row >= end || row / per == (end - 1) / per;   // (a slot stays in one group)
+    if (one_group(s)) {   // closes its group after its rows, also if it has none
+      ++gates_written[group];
     } else {   // a group is closed at its last row
       for (int64_t r = row; r < end; ++r) gates_written[r / per] += (r + 1) % per == 0 || r + 1 == end;
     }
