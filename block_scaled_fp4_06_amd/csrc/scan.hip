@@ -13,7 +13,9 @@
 //  * A tile is 128 bytes of channels (16 lanes of 8 bytes) by kTile time steps: each of 256
 //    threads holds kSteps consecutive steps of its channels in registers.  A run of steps
 //    acts on the state as h -> A h + B; the threads' (A, B) are composed through LDS.
-//  * The tiles of a sequence run in one kernel, so everything is read once.  A workgroup
+//  * The tiles of a sequence run in one kernel, so everything is read once: the decoupled
+//    look-back of Merrill and Garland, "Single-pass Parallel Prefix Scan with Decoupled
+//    Look-back" (2016), over maps of a state instead of sums.  A workgroup
 //    takes the next tile of its strip (a count in memory), so that it only ever waits for
 //    tiles that workgroups already run; it tells the others the tile's (A, B) if it has to
 //    wait, and the state behind the tile as soon as it knows it, each in one 64-bit word.
@@ -28,7 +30,7 @@
 // Few steps (up to kShort) need no tiles: a thread walks over them.
 //
 // Measured in bf16: forward with resets 8192 x 5120 in 68 us, 3.7 TB/s; backward with a
-// floor, 4 x 2048 x 5120, in 113 us, 4.5 TB/s (a copy reaches 5.1); forward with a floor, 6 x
+// floor, 4 x 2048 x 5120, in 112 us, 4.5 TB/s (a copy reaches 5.4); forward with a floor, 6 x
 // 800 x 8031, 52 us, 4.4 TB/s.  The rest is one tile's way through load, LDS, chain and store
 // with 3 workgroups to a CU: 4 gain nothing, tiles of half the steps took a third longer, and
 // more steps a thread do not fit in its registers.  16 bytes a lane, 4 steps: as fast, with
@@ -151,13 +153,24 @@ __device__ __forceinline__ void sigmoids(float g, float &s, float &sc) {
   sc = g < 0.0f ? 1.0f - s : e * s;
 }
 
-// The decay a = floor + (1 - floor) sigmoid(g) and 1 - a.
+// The decay a = floor + (1 - floor) sigmoid(g) and 1 - a.  For bf16 without a selection (6 x
+// 800 x 8031 forward 63 us, 64.5 with): 4 exp(-g) is infinite from where the quotient would
+// be subnormal, which the instruction flushes to zero, so exp(-g) sigmoid(g) is either right
+// or NaN, infinity times zero, which the minimum takes for its end.  (A NaN gate is one in a.)
 template <bool F32, bool FLOOR>
 __device__ __forceinline__ void decay(float g, float fl, float &a, float &w) {
-  float s, sc;
-  sigmoids<F32>(g, s, sc);
-  a = FLOOR ? __builtin_fmaf(1.0f - fl, s, fl) : s;
-  w = FLOOR ? (1.0f - fl) * sc : sc;
+  const float rest = 1.0f - fl;
+  float s;
+  if constexpr (F32) {
+    float sc;
+    sigmoids<F32>(g, s, sc);
+    w = FLOOR ? rest * sc : sc;
+  } else {
+    const float e4 = __builtin_amdgcn_exp2f(__builtin_fmaf(g, -0x1.715476p+0f, 2.0f));
+    s = __builtin_amdgcn_rcpf(__builtin_fmaf(e4, 0.25f, 1.0f));
+    w = (FLOOR ? 0.25f * rest : 0.25f) * __builtin_fminf(e4 * s, 4.0f);
+  }
+  a = FLOOR ? __builtin_fmaf(rest, s, fl) : s;
 }
 
 __device__ __forceinline__ float cut_mark() { return -0.0f; }
@@ -334,13 +347,10 @@ __device__ __forceinline__ bool look(const uint64_t *own, int64_t j, float &befo
 // The chain.  In wave 0, lane = place: from the tile's pair to the state before it, and what
 // other tiles need to know of both.  `given` is the state before the first tile.  States
 // follow from the one before by one pair, in order, however many of those a tile applies
-// itself: results do not depend on who was first.  `in_place`: the state after the last tile
-// takes the place of the one before the first, so the last tile also waits for the first one's
-// word, which that tells only when it has read the state (behind a cut, nothing else would
-// make it wait for that).
+// itself: results do not depend on who was first.
 template <int CH>
 __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t strip, int64_t j, const Pair &all,
-                                                   float given, bool in_place) {
+                                                   float given) {
   const bool live = threadIdx.x < CH, more = j + 1 < t.chunks;
   uint64_t *own = t.words + (strip * t.chunks + j) * CH + threadIdx.x % CH;
   float before = given;
@@ -357,16 +367,24 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
       }
     }
   }
-  if (in_place && !more && j > 0) {
-    const uint64_t *first = own - j * CH;
-    for (int looks = 0; __any(load_agent(first) == 0ull); __builtin_amdgcn_s_sleep(1))
-      if (++looks == kLooks) {   // (never, as above)
-        before = __uint_as_float(0x7FC00000u);
-        break;
-      }
-  }
   if (live && more) store_agent(own, word_of(Pair{cut_mark(), apply(all, before)}));
   return before;
+}
+
+// Whether (it waits until) the first tile of the strip has told its words of this thread's
+// channels: it then has read the state before it, which is told after that.  For a last tile
+// that puts the state after it in that state's place; behind a cut nothing else makes it wait.
+template <int V>
+__device__ __forceinline__ bool first_tile_has_read(const Tiling &t, int64_t strip) {
+  const uint64_t *w = t.words + strip * t.chunks * (kLanes * V) + (threadIdx.x % kLanes) * V;
+  for (int looks = 0; looks < kLooks; ++looks) {   // (ends as the chain's waits do)
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < V; ++i) all &= load_agent(w + i) != 0ull;
+    if (all) return true;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  return false;
 }
 
 // The state before each thread's steps from compose()'s result and the state before the
@@ -374,7 +392,7 @@ __device__ __forceinline__ float state_before_tile(const Tiling &t, int64_t stri
 template <int V, bool PART>
 __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const Tiling &t, const float *given,
                                                  const Spot &at, int64_t j, int64_t first, int64_t chan,
-                                                 float (&h)[V], bool in_place = false) {
+                                                 float (&h)[V]) {
   constexpr int CH = kLanes * V, kSegs = Shared<CH>::kSegs;
   const int tid = threadIdx.x, group = tid / kLanes, lane = tid % kLanes;
   if (tid < 64) {
@@ -388,7 +406,7 @@ __device__ __forceinline__ void states_of_groups(Shared<kLanes * V> &sh, const T
       if (!PART || own) before = given[at.batch * chan + c];
       asm volatile("" : "+v"(before) : : "memory");   // (waits here: the chain's stores come after)
     }
-    if (t.chunks > 1) before = state_before_tile<CH>(t, at.strip, j, all, before, in_place);
+    if (t.chunks > 1) before = state_before_tile<CH>(t, at.strip, j, all, before);
     if (tid < CH) {
 #pragma unroll
       for (int s = 0; s < kSegs; ++s) {
@@ -501,7 +519,7 @@ __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Til
   }
   compose<V, CH>(sh, p);
   float h[V];
-  states_of_groups<V, PART>(sh, tl, a.h0, spot, j, pl.first, a.chan, h, a.h0 && a.h0 == a.h_last);
+  states_of_groups<V, PART>(sh, tl, a.h0, spot, j, pl.first, a.chan, h);
   char *py = at<F32>(a.y, batch * a.y_batch + st.t0 * a.y_time + pl.col);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
@@ -515,10 +533,14 @@ __device__ __forceinline__ void forward_tile(const nvfp4_scan_args &a, const Til
     }
     store<WHOLE, F32>(at<F32>(py, s * a.y_time), pl.own, pl.cnt, h);
   }
-  if (a.h_last && st.more > 0 && st.at + st.more == a.time)
+  if (a.h_last && st.more > 0 && st.at + st.more == a.time) {
+    if (a.h_last == a.h0 && j > 0 && !first_tile_has_read<V>(tl, spot.strip))
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i >= pl.own && i < pl.cnt) a.h_last[batch * a.chan + pl.col + i] = h[i];
+  }
 }
 
 // (One branch for a workgroup: no lane of most tiles has anything to check.)
