@@ -309,7 +309,8 @@ nvfp4_status nvfp4_adamw_step(const void *table, const void *table_device,
   if (p->step < 1 || p->step > 0xFFFFFFFFll) return NVFP4_ERR_SHAPE;
   // (a NaN fails these)
   if (!(p->beta1 >= 0.0 && p->beta1 < 1.0) || !(p->beta2 >= 0.0 && p->beta2 < 1.0) ||
-      !(p->eps >= 0.0 && p->eps < 1e30) || !isfinite(p->lr))
+      !(p->eps >= 0.0 && p->eps < 1e30) || !isfinite(p->lr) ||
+      (h->state_bits == 8 && p->beta1 > NVFP4_ADAMW_MAX_BETA1_8))
     return NVFP4_ERR_UNSUPPORTED;
   if (h->chunks == 0) return NVFP4_OK;
   if (!table_device || !grads) return NVFP4_ERR_NULL;

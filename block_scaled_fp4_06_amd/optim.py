@@ -10,9 +10,10 @@ stochastically (``stochastic_rounding=True``: small updates survive on average).
 The moments of all parameters live in flat buffers (``AdamWState``), each parameter's share
 beginning at a multiple of 256 elements.  8-bit moments hold, per block of 256 elements of a
 parameter, one float32 scale (a power of two) and a byte per element: E4M3 codes for the first
-moment, and for the second the root of v as an unsigned float of 4 exponent and 4 mantissa bits, rounded
-stochastically (rounding to nearest would freeze it: beta2 near 1 moves v by less than half a
-code per step).  The draws come from Philox4x32-10 keyed on (seed, step, parameter, element),
+moment (nearest, so beta1 is at most 17/18: above, a moment whose gradient has vanished would
+stay while the second one decays, and its parameter run away), and for the second the root of v as an unsigned float of 4 exponent and 4
+mantissa bits, rounded stochastically (rounding to nearest would freeze it: beta2 near 1 moves v
+by less than half a code per step).  The draws come from Philox4x32-10 keyed on (seed, step, parameter, element),
 so a step's result is a function of its inputs alone.
 
 The step number and lr are arguments of the launch: a captured HIP graph of a step would
@@ -28,6 +29,7 @@ from . import nvfp4 as N
 from .launch import check, dtype_code, ptr, run_on
 
 BLOCK = 256   # elements of one block of 8-bit moments (NVFP4_ADAMW_BLOCK)
+MAX_BETA1_8 = 17.0 / 18.0   # of 8-bit moments (NVFP4_ADAMW_MAX_BETA1_8)
 
 
 @dataclass
@@ -103,6 +105,9 @@ class AdamW:
         self.stochastic_rounding, self.seed = bool(stochastic_rounding), int(seed)
         self.state = state if state is not None else new_state(self.params, bits, master)
         self._check_state()
+        if self.state.bits == 8 and self.betas[0] > MAX_BETA1_8:
+            raise ValueError("betas[0] is %r, at most 17/18 is supported with 8-bit moments" %
+                             (self.betas[0],))
         self._pack = Struct("=%dQ" % len(self.params)).pack
         self._table = None
 

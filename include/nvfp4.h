@@ -274,8 +274,9 @@ nvfp4_status mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, const u
  * Operators around the linear layers of a training step (the pages' model is a hybrid
  * Mamba-Transformer, [NV-blog] recipe results): the norms, gate and residual sum between
  * blocks, a gated linear recurrence over time, and the AdamW update.  All statistics,
- * sums and states are binary32.  Sizes are arbitrary (no multiples required), pointers
- * need only their element's alignment; 16-byte aligned rows run the wide-load kernels.
+ * sums and states are binary32.  Sizes are arbitrary (no multiples required).  Pointers need
+ * only their element's alignment, and one path serves every alignment; workspaces, the AdamW
+ * table, its moments and the outputs of nvfp4_adamw_moments need 16 bytes.
  * ---------------------------------------------------------------------------------- */
 
 typedef enum { NVFP4_DT_BF16 = 0, NVFP4_DT_FP32 = 1 } nvfp4_dtype;
@@ -435,7 +436,11 @@ nvfp4_status nvfp4_gated_scan_backward(const nvfp4_scan_args *a, const nvfp4_sca
  *
  * Moments in 32 bits, or in 8 bits over blocks of 256 elements of a tensor (the last one
  * may be shorter), each with one binary32 scale:
- *   first:  E4M3 code * scale, nearest-even;
+ *   first:  E4M3 code * scale, nearest-even, which needs beta1 <= 17/18: above, a moment of
+ *           1 1/8 times a power of two is not moved by a gradient of zero, while the second
+ *           moment decays, so the updates grow without end.  (Below, this holds for the smallest
+ *           codes alone, up to 4 at beta1 = 0.9, 2^-14 of the block's largest moment: where
+ *           the rest of a block goes on, such an element moves by up to about 2 lr a step.);
  *   second: the root r = sqrt(v) as value(code) * scale with value(c) = 2 f for e = 0 and
  *           (16 + f) 2^e otherwise, e = c >> 4, f = c & 15; rounded stochastically (with
  *           beta2 near 1 a step moves v by less than half a code, so rounding to nearest
@@ -451,6 +456,7 @@ nvfp4_status nvfp4_gated_scan_backward(const nvfp4_scan_args *a, const nvfp4_sca
  * moment and 1 for the parameter.
  */
 #define NVFP4_ADAMW_BLOCK 256
+#define NVFP4_ADAMW_MAX_BETA1_8 (17.0 / 18.0)
 
 typedef struct {
     void *param;            /* (device) n elements */
@@ -465,7 +471,7 @@ typedef struct {
 } nvfp4_adamw_tensor;
 
 typedef struct {
-    double lr, beta1, beta2, eps;
+    double lr, beta1, beta2, eps; /* beta1 <= NVFP4_ADAMW_MAX_BETA1_8 with 8-bit moments */
     int64_t step;           /* 1 for the first update */
     uint64_t seed;          /* of the stochastic rounding */
     int32_t stochastic_param; /* 1: bf16 parameters are rounded stochastically */
