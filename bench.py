@@ -100,8 +100,9 @@ def to_dev(x_u16):
 
 
 def copy_bandwidth(nbuf_bytes=512 << 20, chunk=84 << 20, iters=30):
-    """Device-to-device copy rate (GB/s, read + write bytes) over rotated buffers: the
-    practical HBM ceiling the quantize rates are also compared with."""
+    """Device-to-device copy rate (GB/s, read + write bytes) from rotated buffers into one,
+    which stays in the Infinity Cache: the ceiling the quantize rates are also compared with
+    (their outputs stay there too)."""
     import torch
     nb = max(2, -(-nbuf_bytes // chunk))
     src = [torch.empty(chunk, dtype=torch.uint8, device="cuda") for _ in range(nb)]

@@ -20,7 +20,7 @@
 // block's two largest magnitudes are maxima over 32 lanes.
 //
 // Measured with 104857600 elements: bf16 weights with fp32 masters and moments 500-554 us,
-// 5.3-5.9 TB/s (a copy between two buffers: 5.1).  8-bit moments and stochastically rounded
+// 5.3-5.9 TB/s (a copy reaches 5.4).  8-bit moments and stochastically rounded
 // bf16 weights 253-283 us a step, 3.7-4.2 TB/s: the rounds of Philox and the correctly
 // rounded roots and divisions bound it, not memory; both moments decoded to bf16 96 us, 6.6
 // TB/s (the codes were just written).  30 tensors of 60001 elements in all: 5.1 us.
