@@ -440,7 +440,7 @@ nvfp4_status nvfp4_gated_scan_backward(const nvfp4_scan_args *a, const nvfp4_sca
  *           1 1/8 times a power of two is not moved by a gradient of zero, while the second
  *           moment decays, so the updates grow without end.  (Below, this holds for the smallest
  *           codes alone, up to 4 at beta1 = 0.9, 2^-14 of the block's largest moment: where
- *           the rest of a block goes on, such an element moves by up to about 2 lr a step.);
+ *           the rest of a block goes on, such an element moves by 2 lr a step, 8 at most.);
  *   second: the root r = sqrt(v) as value(code) * scale with value(c) = 2 f for e = 0 and
  *           (16 + f) 2^e otherwise, e = c >> 4, f = c & 15; rounded stochastically (with
  *           beta2 near 1 a step moves v by less than half a code, so rounding to nearest
