@@ -17,6 +17,7 @@ from typing import Optional
 from . import linear as L
 from . import norm
 from . import recurrence as R
+from .launch import run_on, tensors_in
 
 
 @dataclass
@@ -65,30 +66,35 @@ def block_forward(x, h, p: BlockParams, batch, time, h0=None, reset=None, sr_see
                   skip_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None):
     """(x_out, h_next, state, ctx); state (batch, dim) float32 is the recurrence's after the
     last step, h0 the one before the first."""
-    dim = x.shape[1]
-    gu, lin_in = L.linear_forward(h, p.w_in, sr_seed=sr_seed, stream=stream)
-    gu = gu.view(batch, time, 2 * dim)
-    y, state = R.gated_scan_forward(gu[:, :, :dim], gu[:, :, dim:], p.floor, h0, reset,
-                                    stream=stream)
-    z, lin_out = L.linear_forward(y.view(batch * time, dim), p.w_out, sr_seed=sr_seed + 2,
-                                  stream=stream)
-    x_out, h_next, ctx = norm.residual_norm_forward(x, z, p.post_weight, p.next_weight, p.gate,
-                                                    skip_scale, branch_scale, eps, stream=stream)
-    return x_out, h_next, state, BlockContext(lin_in, lin_out, gu, y, p.floor, h0, reset, ctx)
+    def call(_):   # (with `stream` current: what lies between the calls belongs to it too)
+        dim = x.shape[1]
+        gu, lin_in = L.linear_forward(h, p.w_in, sr_seed=sr_seed)
+        gu = gu.view(batch, time, 2 * dim)
+        y, state = R.gated_scan_forward(gu[:, :, :dim], gu[:, :, dim:], p.floor, h0, reset)
+        z, lin_out = L.linear_forward(y.view(batch * time, dim), p.w_out, sr_seed=sr_seed + 2)
+        x_out, h_next, ctx = norm.residual_norm_forward(x, z, p.post_weight, p.next_weight, p.gate,
+                                                        skip_scale, branch_scale, eps)
+        return x_out, h_next, state, BlockContext(lin_in, lin_out, gu, y, p.floor, h0, reset, ctx)
+    used = () if stream is None else list(tensors_in(x, h, p, h0, reset))
+    return run_on(stream, x.device, used, call)
 
 
 def block_backward(dx_out, dh_next, ctx: BlockContext, dstate=None, stream=None):
     """(dx, dh, dh0, gradients as a BlockParams) from the gradients of block_forward's
     results (dx_out None: zero; dstate None: zero)."""
     import torch
-    batch, time, dim = ctx.y.shape
-    d = norm.residual_norm_backward(dx_out, dh_next, ctx.norm, stream=stream)
-    dy, dw_out = L.linear_backward(d.dz, ctx.lin_out, dw_dtype=torch.bfloat16, stream=stream)
-    dgu = torch.empty_like(ctx.gu)
-    g, u = ctx.gu[:, :, :dim], ctx.gu[:, :, dim:]
-    s = R.gated_scan_backward(dy.view(batch, time, dim), g, u, ctx.y, ctx.floor, ctx.h0, ctx.reset,
-                              dstate, stream=stream, out=(dgu[:, :, :dim], dgu[:, :, dim:]))
-    dh, dw_in = L.linear_backward(dgu.view(batch * time, 2 * dim), ctx.lin_in,
-                                  dw_dtype=torch.bfloat16, stream=stream)
-    grads = BlockParams(dw_in, dw_out, s.dfloor, d.dpost_weight, d.dgate, d.dnext_weight)
-    return d.dx, dh, s.dh0, grads
+
+    def call(_):
+        batch, time, dim = ctx.y.shape
+        d = norm.residual_norm_backward(dx_out, dh_next, ctx.norm)
+        dy, dw_out = L.linear_backward(d.dz, ctx.lin_out, dw_dtype=torch.bfloat16)
+        dgu = torch.empty_like(ctx.gu)
+        g, u = ctx.gu[:, :, :dim], ctx.gu[:, :, dim:]
+        s = R.gated_scan_backward(dy.view(batch, time, dim), g, u, ctx.y, ctx.floor, ctx.h0,
+                                  ctx.reset, dstate, out=(dgu[:, :, :dim], dgu[:, :, dim:]))
+        dh, dw_in = L.linear_backward(dgu.view(batch * time, 2 * dim), ctx.lin_in,
+                                      dw_dtype=torch.bfloat16)
+        grads = BlockParams(dw_in, dw_out, s.dfloor, d.dpost_weight, d.dgate, d.dnext_weight)
+        return d.dx, dh, s.dh0, grads
+    used = () if stream is None else list(tensors_in(dx_out, dh_next, ctx, dstate))
+    return run_on(stream, ctx.y.device, used, call)

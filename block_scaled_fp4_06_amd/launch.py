@@ -2,6 +2,8 @@
 the memory it takes there, and the checks of its tensors."""
 from __future__ import annotations
 
+from dataclasses import fields, is_dataclass
+
 from . import nvfp4 as N
 
 _CODES = {}
@@ -42,6 +44,16 @@ def run_on(stream, device, inputs, call):
             if t is not None:
                 t.record_stream(stream)
         return call(stream.cuda_stream)
+
+
+def tensors_in(*parts):
+    """The tensors among `parts` and in the fields of their dataclasses."""
+    import torch
+    for p in parts:
+        if isinstance(p, torch.Tensor):
+            yield p
+        elif is_dataclass(p):
+            yield from tensors_in(*(getattr(p, f.name) for f in fields(p)))
 
 
 def check(rc, name):
