@@ -25,6 +25,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 from . import nvfp4 as N
+from .launch import run_on, tensors_in
 
 DEFAULT_RHT_SEED = 0x5248
 
@@ -41,24 +42,31 @@ class LinearContext:
 def linear_forward(x, w, rht_seed: int = DEFAULT_RHT_SEED, sr_seed: int = 0, out_dtype=None,
                    stream=None):
     """Y = X W for bf16 x (M, K) and w (K, N); returns (y, ctx)."""
-    qx = N.quantize(x, blocking="1x16", rounding="rne", stream=stream)
-    qw = N.quantize(w, blocking="16x16", rounding="rne", with_transpose=True, stream=stream)
-    y = N.gemm(qx, qw.transposed(), out_dtype=out_dtype, stream=stream)
-    return y, LinearContext(x, qw, rht_seed, sr_seed)
+    def call(_):   # (with `stream` current: what lies between the calls belongs to it too)
+        qx = N.quantize(x, blocking="1x16", rounding="rne")
+        qw = N.quantize(w, blocking="16x16", rounding="rne", with_transpose=True)
+        y = N.gemm(qx, qw.transposed(), out_dtype=out_dtype)
+        return y, LinearContext(x, qw, rht_seed, sr_seed)
+    if stream is None:
+        return call(None)
+    return run_on(stream, x.device, [x, w], call)
 
 
 def linear_backward(dy, ctx: LinearContext, dx_dtype=None, dw_dtype=None, stream=None):
     """(dX, dW) for the bf16 output gradient dy (M, N)."""
-    qdy = N.quantize(dy, blocking="1x16", rounding="sr", sr_seed=ctx.sr_seed, stream=stream)
-    dx = N.gemm(qdy, ctx.qw, out_dtype=dx_dtype, stream=stream)
-    xt = N.transpose(ctx.x, stream=stream)
-    dyt = N.transpose(dy, stream=stream)
-    qxt = N.quantize(xt, blocking="1x16", rounding="rne", rht=True, rht_seed=ctx.rht_seed,
-                     stream=stream)
-    qdyt = N.quantize(dyt, blocking="1x16", rounding="sr", rht=True, rht_seed=ctx.rht_seed,
-                      sr_seed=ctx.sr_seed + 1, stream=stream)
-    dw = N.gemm(qxt, qdyt, out_dtype=dw_dtype, stream=stream)
-    return dx, dw
+    def call(_):
+        qdy = N.quantize(dy, blocking="1x16", rounding="sr", sr_seed=ctx.sr_seed)
+        dx = N.gemm(qdy, ctx.qw, out_dtype=dx_dtype)
+        xt = N.transpose(ctx.x)
+        dyt = N.transpose(dy)
+        qxt = N.quantize(xt, blocking="1x16", rounding="rne", rht=True, rht_seed=ctx.rht_seed)
+        qdyt = N.quantize(dyt, blocking="1x16", rounding="sr", rht=True, rht_seed=ctx.rht_seed,
+                          sr_seed=ctx.sr_seed + 1)
+        dw = N.gemm(qxt, qdyt, out_dtype=dw_dtype)
+        return dx, dw
+    if stream is None:
+        return call(None)
+    return run_on(stream, dy.device, list(tensors_in(dy, ctx)), call)
 
 
 _AUTOGRAD_FN = None
