@@ -97,10 +97,15 @@ def _args(g, u, floor, h0, reset, y, h_last):
 
 def gated_scan_forward(g, u, floor=None, h0=None, reset=None, h_last=None, stream=None):
     """(y, h_last): every step's state in the type of g, and the last one in float32 (into
-    h_last where given; h0 itself for a state kept in place)."""
+    h_last where given: h0 itself for a state kept in place, or memory of no input)."""
     import torch
     (batch, time, chan), _, dev = _check_inputs(g, u, floor, h0, reset)
     _plain("h_last", h_last, (batch, chan), (torch.float32,), dev)
+    if h_last is not None and h_last is not h0:
+        for name, t in (("h0", None if ptr(h0) == ptr(h_last) else h0), ("g", g), ("u", u),
+                        ("floor", floor), ("reset", reset)):
+            if not apart(h_last, t):
+                raise ValueError("h_last shares memory with %s" % name)
     given = h_last
 
     def call(handle):

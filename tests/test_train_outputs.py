@@ -97,3 +97,13 @@ def test_norm_sum_given(no_library_calls):  # noqa: F811
                      (dict(out=x), "GPU"), (dict(out=buf[:6]), "GPU"), (dict(out=torch.zeros(6, 32)), "GPU")):
         with pytest.raises(ValueError, match=what):
             norm.residual_norm_forward(**dict(dict(x=x, z=z, post_weight=w, next_weight=w), **kw))
+
+
+def test_scan_state_given(no_library_calls):  # noqa: F811
+    g, buf = torch.zeros(2, 5, 8), torch.zeros(5, 8)
+    h0 = buf[1:3]
+    for last, what in ((buf[2:4], "memory with h0"), (buf[:2], "memory with h0"),
+                       (g.view(-1)[:16].view(2, 8), "memory with g"), (buf[1:3], "GPU"), (h0, "GPU"),
+                       (buf[3:], "GPU"), (torch.zeros(2, 8), "GPU")):
+        with pytest.raises(ValueError, match=what):
+            R.gated_scan_forward(g, g.clone(), None, h0, h_last=last)
