@@ -128,12 +128,12 @@ __device__ __forceinline__ void load_f32(const float *p, int64_t i, int cnt, flo
 }
 
 // ---------------------------------------------------------------- arithmetic
-// exp(-g).  A product with log2(e) in 24 bits is off by up to |g| 2^-25 before the
-// exponential, which bf16 results do not notice (|g| up to 2^15 still leaves their rounding the
-// larger error where the result is not zero).  binary32 gets the product's error back as a
-// factor: for |g| of 20 to 40 sigmoid(-g) is off by 3.6e-8 (rms), 8.4e-7 without.  (Clamped
-// to where it is zero, and to log(2^128), where it is infinite: both products stay finite and
-// the factor of the infinite one positive.)
+// exp(-g).  A product with log2(e) in 24 bits is off by up to |g| 2^-24 before the
+// exponential, which bf16 results do not notice (4e-6 of the result at most where it is not
+// zero, their own rounding 2e-3).  binary32 gets the product's error back as a factor: for
+// |g| of 20 to 40 sigmoid(-g) is off by 3.6e-8 (rms), 8.4e-7 without.  (Clamped to where it
+// is zero, and to log(2^128), where it is infinite: both products stay finite and the factor
+// of the infinite one positive.)
 template <bool F32>
 __device__ __forceinline__ float exp_minus(float g) {
   if constexpr (!F32) return __expf(-g);
